@@ -245,6 +245,86 @@ MUON_API int muon_adamw_step(float* const* params, const float* const* grads,
                              int64_t step, double lr, double beta1, double beta2, double eps,
                              double weight_decay, void* stream);
 
+/*
+ * Gradient clipping.  One norm over every gradient of a model, whichever
+ * optimizer steps it, and the gradients scaled by it:
+ *
+ *   N = (sum over all tensors and entries of |g|^p)^(1/p)   p = 1 or 2
+ *   N = the largest |g|                                     p = INFINITY
+ *   s = min(1, max_norm / (N + eps))
+ *
+ * Clipping is part of the training loop of "Let's reproduce GPT-2 (124M)"; the
+ * page gives no formulas, these are the usual ones.
+ *
+ *   grads   host pointer array [n] of device tensors, contiguous; dtypes[i]
+ *           is the muon_dtype_t of grads[i] (types may be mixed) and
+ *           numels[i] its element count (0 skips it; at most 2^40).
+ *           Pointers need only be aligned to their element.
+ *   p       1, 2 or INFINITY.
+ *   max_norm  >= 0; INFINITY gives s = 1.      eps  >= 0, finite.
+ *   norm    device float (4-byte aligned): N, rounded once to fp32.
+ *   scale   device float or NULL: s, formed in fp64 and rounded once.
+ *   workspace  device memory, 8-byte aligned, of at least
+ *           muon_grad_workspace_bytes() bytes; needs no initialisation and
+ *           holds nothing after the call.  Calls whose executions may overlap
+ *           on the GPU (other streams, other graphs) need workspaces and
+ *           results of their own; the library shares nothing between them.
+ *   stream  cudaStream_t as void*.
+ *
+ * Squares and sums are fp64, in a fixed order: nothing underflows or
+ * overflows for finite fp32 input unless N itself does, and the same call on
+ * the same device gives the same bits.  NaN and infinity go as the formulas
+ * say: an infinite N gives s = 0 (and so NaN in the entries that were
+ * infinite), a NaN N gives s = NaN.  N + eps = 0 gives s = 1.  With n = 0, or
+ * only empty tensors, N is 0 and is still written.
+ */
+typedef enum { MUON_F32 = 0, MUON_BF16 = 1, MUON_F16 = 2 } muon_dtype_t;
+
+/* muon_grad_workspace_bytes -- workspace of the two calls below for these
+ * tensors (host-only computation; -1 on a bad argument). */
+MUON_API int64_t muon_grad_workspace_bytes(const unsigned char* dtypes, const int64_t* numels, int n);
+
+/* muon_grad_norm -- N and s; the gradients are only read. */
+MUON_API int muon_grad_norm(const void* const* grads, const unsigned char* dtypes,
+                            const int64_t* numels, int n, double p, double max_norm, double eps,
+                            float* norm, float* scale, void* workspace, int64_t workspace_bytes,
+                            void* stream);
+
+/* muon_clip_grads -- the same, and outs[i] = s * grads[i]: the product rounded
+ * to fp32 and then, for a 16-bit out, to its type.  outs[i] with its type
+ * out_dtypes[i] is either grads[i] itself with the same type (in place; left
+ * untouched when s is exactly 1) or overlaps no gradient and no other out.
+ * outs = NULL is muon_grad_norm. */
+MUON_API int muon_clip_grads(const void* const* grads, const unsigned char* dtypes,
+                             const int64_t* numels, int n, void* const* outs,
+                             const unsigned char* out_dtypes, double p, double max_norm, double eps,
+                             float* norm, float* scale, void* workspace, int64_t workspace_bytes,
+                             void* stream);
+
+/*
+ * The steps with the scale applied on the way: every gradient entry is first
+ * multiplied by *grad_scale (a device float, 4-byte aligned, read when the
+ * kernel runs; the product rounded to fp32), so the result equals clipping
+ * the fp32 gradients in memory and then stepping, bit for bit, without writing
+ * them and reading them back.  grad_scale = NULL is the plain call.  A NaN
+ * scale makes every state and parameter of the call NaN: read N first where
+ * such a step is to be skipped.  Other arguments as in the plain calls;
+ * mirrors may be NULL with n_mirrors = 0.
+ */
+MUON_API int muon_step_scaled(float* const* params, const float* const* grads, float* const* bufs,
+                              const int64_t* shapes, int n, float lr, float beta, int nesterov,
+                              int ns_steps, const float* coeffs, float* const* mirrors,
+                              int n_mirrors, const float* grad_scale, void* stream);
+MUON_API int muon_adamw_step_scaled(float* const* params, const float* const* grads,
+                                    float* const* exp_avgs, float* const* exp_avg_sqs,
+                                    const int64_t* numels, const unsigned char* decay, int n,
+                                    int64_t step, double lr, double beta1, double beta2, double eps,
+                                    double weight_decay, const float* grad_scale, void* stream);
+MUON_API int muon_momentum_normalize_scaled(const float* const* grads, float* const* bufs,
+                                            uint16_t* const* x0, const int64_t* x0_ld,
+                                            const int64_t* shapes, int n, float beta, int nesterov,
+                                            const float* grad_scale, void* stream);
+
 /* muon_status -- synchronises the stream, then returns (and clears) the
  * device-side status of the current device: MUON_OK or MUON_ERR_TIMEOUT;
  * MUON_ERR_CUDA if the synchronisation itself failed. */
@@ -275,10 +355,11 @@ MUON_API int64_t muon_workspace_bytes(const int64_t* shapes, int n);
  *   7 the chain launch: every Gram, polynomial and X-update phase of a step
  *     but the last update (kinds 1-3 are then used only by the stage entry
  *     points)
+ *   8 gradient norm   9 gradient scaling (muon_clip_grads)
  * ms and launches are host arrays of at least nkinds entries.  Returns the
  * number of kinds written, or a negative status.
  */
-#define MUON_PROFILE_KINDS 8
+#define MUON_PROFILE_KINDS 10
 MUON_API void muon_profile_begin(void);
 MUON_API int muon_profile_end(double* ms, int64_t* launches, int nkinds);
 

@@ -21,6 +21,7 @@ __all__ = [
     "DEFAULT_COEFFS", "MuonError", "library", "step", "orthogonalize", "momentum_normalize",
     "gram", "poly", "xupdate", "status", "release", "workspace_bytes", "set_wait_limit_ns",
     "adamw_step", "AdamWGroup", "capture_step", "EXPORTS", "guard_check",
+    "grad_norm", "clip_scale", "clip_grads", "GradGroup",
 ]
 
 DEFAULT_COEFFS = (3.4445, -4.7750, 2.0315)
@@ -31,10 +32,12 @@ EXPORTS = ("muon_step", "muon_orthogonalize", "muon_momentum_normalize", "muon_g
            "muon_xupdate", "muon_status", "muon_error_string", "muon_set_wait_limit_ns",
            "muon_workspace_bytes", "muon_release", "muon_version", "muon_profile_begin",
            "muon_profile_end", "muon_momentum_normalize_noalloc", "muon_adamw_step",
-           "muon_step_mirrored", "muon_guard_check")
+           "muon_step_mirrored", "muon_guard_check", "muon_grad_workspace_bytes", "muon_grad_norm",
+           "muon_clip_grads", "muon_step_scaled", "muon_adamw_step_scaled",
+           "muon_momentum_normalize_scaled")
 
 PROFILE_KINDS = ("momentum_norm_cast", "gram", "poly", "xupdate", "xupdate_final", "apply", "adamw",
-                 "ns_chain")
+                 "ns_chain", "grad_norm", "grad_scale")
 
 _STATUS = {0: "MUON_OK", -1: "MUON_ERR_INVALID_ARG", -2: "MUON_ERR_UNSUPPORTED",
            -3: "MUON_ERR_CUDA", -4: "MUON_ERR_NOMEM", -5: "MUON_ERR_TIMEOUT"}
@@ -82,6 +85,12 @@ def library() -> ctypes.CDLL:
         "muon_adamw_step": (i, [_PP, _PP, _PP, _PP, _I64P, _P, i, i64, d, d, d, d, d, _P]),
         "muon_step_mirrored": (i, [_PP, _PP, _PP, _I64P, i, f, f, i, i, _FP, _PP, i, _P]),
         "muon_guard_check": (i64, []),
+        "muon_grad_workspace_bytes": (i64, [_P, _I64P, i]),
+        "muon_grad_norm": (i, [_PP, _P, _I64P, i, d, d, d, _P, _P, _P, i64, _P]),
+        "muon_clip_grads": (i, [_PP, _P, _I64P, i, _PP, _P, d, d, d, _P, _P, _P, i64, _P]),
+        "muon_step_scaled": (i, [_PP, _PP, _PP, _I64P, i, f, f, i, i, _FP, _PP, i, _P, _P]),
+        "muon_adamw_step_scaled": (i, [_PP, _PP, _PP, _PP, _I64P, _P, i, i64, d, d, d, d, d, _P, _P]),
+        "muon_momentum_normalize_scaled": (i, [_PP, _PP, _PP, _I64P, _I64P, i, f, i, _P, _P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -112,6 +121,24 @@ def _coeffs(coeffs):
     return (ctypes.c_float * 3)(*[float(c) for c in coeffs])
 
 
+def _scale_ptr(grad_scale):
+    """Device address of a gradient scale (a one-element fp32 CUDA tensor on
+    the current device), or None."""
+    if grad_scale is None:
+        return None
+    if not isinstance(grad_scale, torch.Tensor) or not grad_scale.is_cuda \
+            or grad_scale.dtype != torch.float32 or grad_scale.numel() != 1:
+        raise ValueError("grad_scale: expected a float32 CUDA tensor of one element")
+    _check_device(grad_scale.device.index, "grad_scale")
+    return grad_scale.data_ptr()
+
+
+def _check_device(index: int, name: str):
+    if index != torch.cuda.current_device():
+        raise ValueError(f"{name}: on cuda:{index}, but the current device is "
+                         f"cuda:{torch.cuda.current_device()}")
+
+
 def _check_mat(t: torch.Tensor, name: str, dtype=torch.float32):
     if not isinstance(t, torch.Tensor) or t.dim() != 2:
         raise ValueError(f"{name}: expected a 2-D tensor")
@@ -134,7 +161,7 @@ def _as_matrix(t: torch.Tensor) -> torch.Tensor:
 def step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor],
          bufs: Sequence[torch.Tensor], lr: float, beta: float = 0.95, nesterov: bool = True,
          ns_steps: int = 5, coeffs=DEFAULT_COEFFS, stream=None, reshape_nd: bool = False,
-         mirrors=None) -> None:
+         mirrors=None, grad_scale: torch.Tensor | None = None) -> None:
     """One Muon step, in place on params and bufs (see include/muon.h).
 
     With reshape_nd, tensors of rank >= 3 (conv weights) are updated as their
@@ -144,6 +171,9 @@ def step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor],
     parameter (a tensor of the same shape, or a raw device address, e.g. of
     another GPU's copy); the last kernel writes every updated matrix to each
     of them as well (muon_step_mirrored).
+
+    grad_scale: optional one-element fp32 CUDA tensor (clip_scale's) that
+    multiplies every gradient on the way in; grads themselves stay as they are.
     """
     n = len(params)
     if len(grads) != n or len(bufs) != n:
@@ -173,22 +203,20 @@ def step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor],
                 else:
                     flat.append(int(t))
         mir = (ctypes.c_void_p * len(flat))(*flat)
-        code = library().muon_step_mirrored(
-            _ptr_array(params), _ptr_array(grads), _ptr_array(bufs), sh, n, float(lr), float(beta),
-            int(bool(nesterov)), int(ns_steps), _coeffs(coeffs), mir, len(mirrors),
-            _stream_ptr(stream))
-        _check(code, "muon_step_mirrored")
-        return
-    code = library().muon_step(_ptr_array(params), _ptr_array(grads), _ptr_array(bufs), sh, n,
-                               float(lr), float(beta), int(bool(nesterov)), int(ns_steps),
-                               _coeffs(coeffs), _stream_ptr(stream))
-    _check(code, "muon_step")
+    else:
+        mir, mirrors = None, ()
+    code = library().muon_step_scaled(
+        _ptr_array(params), _ptr_array(grads), _ptr_array(bufs), sh, n, float(lr), float(beta),
+        int(bool(nesterov)), int(ns_steps), _coeffs(coeffs), mir, len(mirrors),
+        _scale_ptr(grad_scale), _stream_ptr(stream))
+    _check(code, "muon_step_mirrored" if mirrors else "muon_step")
 
 
 def capture_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor],
                  bufs: Sequence[torch.Tensor], lr: float, beta: float = 0.95,
                  nesterov: bool = True, ns_steps: int = 5, coeffs=DEFAULT_COEFFS,
-                 reshape_nd: bool = False) -> "torch.cuda.CUDAGraph":
+                 reshape_nd: bool = False,
+                 grad_scale: torch.Tensor | None = None) -> "torch.cuda.CUDAGraph":
     """Run one Muon step eagerly, then capture the next one in a CUDA graph.
 
     The first call for a set of shapes and parameter pointers builds the
@@ -197,11 +225,12 @@ def capture_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor],
     before capturing.  Every ``replay()`` of the returned graph is one more
     step on the same tensors: write each step's gradients into ``grads`` in
     place before replaying.  The graph keeps the hyper-parameters it was
-    captured with.  Launching nothing but kernels and one memset, a replay
+    captured with, but reads ``grad_scale`` (when given) anew each time: write
+    each step's scale into that tensor before replaying.  Launching nothing but kernels and one memset, a replay
     saves the host work and launch gaps of the eager call.
     """
     kw = dict(lr=lr, beta=beta, nesterov=nesterov, ns_steps=ns_steps, coeffs=coeffs,
-              reshape_nd=reshape_nd)
+              reshape_nd=reshape_nd, grad_scale=grad_scale)
     step(params, grads, bufs, **kw)
     torch.cuda.synchronize()
     _check(status(), "muon_step (before capture)")
@@ -226,11 +255,14 @@ def step_raw(param_ptrs, grad_ptrs, buf_ptrs, shapes, lr, beta=0.95, nesterov=Tr
 def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor],
                exp_avgs: Sequence[torch.Tensor], exp_avg_sqs: Sequence[torch.Tensor], step: int,
                lr: float, betas=(0.9, 0.999), eps: float = 1e-8, weight_decay: float = 1e-2,
-               decay: Sequence[bool] | None = None, stream=None) -> None:
+               decay: Sequence[bool] | None = None, stream=None,
+               grad_scale: torch.Tensor | None = None) -> None:
     """One AdamW step, in place on params and both running averages (see
     include/muon.h).  Tensors: fp32, contiguous, on the GPU, any shape; the
     four lists match element by element.  ``decay[i]`` false puts tensor i in
-    the no-decay group; ``decay=None`` decays all.  ``step`` counts from 1."""
+    the no-decay group; ``decay=None`` decays all.  ``step`` counts from 1.
+    ``grad_scale``: optional one-element fp32 CUDA tensor (clip_scale's) that
+    multiplies every gradient on the way in."""
     n = len(params)
     if not (len(grads) == len(exp_avgs) == len(exp_avg_sqs) == n):
         raise ValueError("params, grads, exp_avgs and exp_avg_sqs must have the same length")
@@ -247,7 +279,8 @@ def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor],
         numels.append(p.numel())
     code = adamw_step_raw([t.data_ptr() for t in params], [t.data_ptr() for t in grads],
                           [t.data_ptr() for t in exp_avgs], [t.data_ptr() for t in exp_avg_sqs],
-                          numels, step, lr, betas, eps, weight_decay, decay, _stream_ptr(stream))
+                          numels, step, lr, betas, eps, weight_decay, decay, _stream_ptr(stream),
+                          _scale_ptr(grad_scale))
     _check(code, "muon_adamw_step")
 
 
@@ -287,28 +320,160 @@ class AdamWGroup:
         self.lr, self.betas, self.eps, self.weight_decay = float(lr), tuple(betas), float(eps), \
             float(weight_decay)
 
-    def step(self, step: int, lr: float | None = None, stream=None) -> None:
-        """One AdamW step (t = ``step``, from 1) on the group's tensors."""
-        code = library().muon_adamw_step(
+    def step(self, step: int, lr: float | None = None, stream=None,
+             grad_scale: torch.Tensor | None = None) -> None:
+        """One AdamW step (t = ``step``, from 1) on the group's tensors;
+        ``grad_scale`` as for adamw_step."""
+        code = library().muon_adamw_step_scaled(
             self._p, self._g, self._m, self._v, self._numels,
             ctypes.cast(self._decay, ctypes.c_void_p) if self._decay is not None else None,
             self._n, int(step), self.lr if lr is None else float(lr), float(self.betas[0]),
-            float(self.betas[1]), self.eps, self.weight_decay, _stream_ptr(stream))
+            float(self.betas[1]), self.eps, self.weight_decay, _scale_ptr(grad_scale),
+            _stream_ptr(stream))
         _check(code, "muon_adamw_step")
 
 
 def adamw_step_raw(param_ptrs, grad_ptrs, avg_ptrs, sq_ptrs, numels, step, lr, betas=(0.9, 0.999),
-                   eps=1e-8, weight_decay=1e-2, decay=None, stream=0) -> int:
-    """muon_adamw_step on raw device pointers; returns the status code unchanged."""
+                   eps=1e-8, weight_decay=1e-2, decay=None, stream=0, grad_scale=None) -> int:
+    """muon_adamw_step on raw device pointers (grad_scale too); returns the status code unchanged."""
     n = len(param_ptrs)
     arr = lambda xs: (ctypes.c_void_p * max(n, 1))(*xs)  # noqa: E731
     ne = (ctypes.c_int64 * max(n, 1))(*[int(x) for x in numels])
     dm = None if decay is None else (ctypes.c_ubyte * max(n, 1))(*[1 if d else 0 for d in decay])
-    return library().muon_adamw_step(arr(param_ptrs), arr(grad_ptrs), arr(avg_ptrs), arr(sq_ptrs), ne,
-                                     ctypes.cast(dm, ctypes.c_void_p) if dm is not None else None, n,
-                                     int(step), float(lr), float(betas[0]), float(betas[1]),
-                                     float(eps), float(weight_decay),
-                                     int(stream) if stream is not None else None)
+    return library().muon_adamw_step_scaled(
+        arr(param_ptrs), arr(grad_ptrs), arr(avg_ptrs), arr(sq_ptrs), ne,
+        ctypes.cast(dm, ctypes.c_void_p) if dm is not None else None, n, int(step), float(lr),
+        float(betas[0]), float(betas[1]), float(eps), float(weight_decay), grad_scale,
+        int(stream) if stream is not None else None)
+
+
+_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
+
+class GradGroup:
+    """A fixed set of gradients for the norm and for clipping, checked and
+    marshalled once (AdamWGroup does the same for its step).
+
+    ``grads``: contiguous CUDA tensors of any shape on one device; float32,
+    bfloat16 and float16 may be mixed, empty ones are skipped.  They must stay
+    allocated at the same addresses for the group's lifetime; their values are
+    read anew by every call.  ``out``: optional tensors of the same shapes, of
+    any of the three types, that ``clip`` writes instead of ``grads`` (bf16
+    gradients into the fp32 ones that the steps take, for instance); an entry
+    may be the gradient itself, none may overlap anything else.
+
+    Every call takes its workspace and its results from torch's allocator on
+    the call's stream, so calls on several streams and captures in several
+    graphs do not disturb one another.  The library's first call on a device
+    allocates; make it before any capture.
+    """
+
+    def __init__(self, grads: Sequence[torch.Tensor], out: Sequence[torch.Tensor] | None = None):
+        n = len(grads)
+        if out is not None and len(out) != n:
+            raise ValueError("grads and out must have the same length")
+        self._device = None
+        for ts, nm in ((grads, "grad"), (out or (), "out")):
+            for t in ts:
+                if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype not in _DTYPES \
+                        or not t.is_contiguous():
+                    raise ValueError(f"{nm}: expected a contiguous float32, bfloat16 or float16 CUDA tensor")
+                if self._device is None:
+                    self._device = t.device.index
+                elif t.device.index != self._device:
+                    raise ValueError("every tensor must be on one device")
+        if out is not None and any(o.shape != g.shape for o, g in zip(out, grads)):
+            raise ValueError("grad and out shapes differ")
+        self._keep = (list(grads), None if out is None else list(out))
+        self._n = n
+        arr = lambda ts: (ctypes.c_void_p * max(n, 1))(*[t.data_ptr() for t in ts])  # noqa: E731
+        kinds = lambda ts: (ctypes.c_ubyte * max(n, 1))(*[_DTYPES[t.dtype] for t in ts])  # noqa: E731
+        self._g, self._gt = arr(grads), kinds(grads)
+        self._o, self._ot = (self._g, self._gt) if out is None else (arr(out), kinds(out))
+        self._numels = (ctypes.c_int64 * max(n, 1))(*[t.numel() for t in grads])
+        self._bytes = int(library().muon_grad_workspace_bytes(self._gt, self._numels, n))
+        if self._bytes < 0:
+            raise ValueError("a gradient is too large")
+        self._clippable = self._disjoint(grads, grads if out is None else out)
+
+    @staticmethod
+    def _disjoint(grads, outs) -> bool:
+        """Whether no output overlaps another output, or a gradient other
+        than its own (of the same type, at the same address)."""
+        spans = []
+        for i, (g, o) in enumerate(zip(grads, outs)):
+            if o.numel() == 0:
+                continue
+            a, b = o.data_ptr(), g.data_ptr()
+            spans.append((a, a + o.numel() * o.element_size(), True))
+            if a != b or o.dtype != g.dtype:
+                spans.append((b, b + g.numel() * g.element_size(), False))
+        spans.sort()
+        ends = {True: 0, False: 0}
+        for a, e, written in spans:
+            if a < ends[True] or (written and a < ends[False]):
+                return False
+            ends[written] = max(ends[written], e)
+        return True
+
+    def _call(self, fn, what, head, p, max_norm, eps, with_scale, stream):
+        if self._device is not None:
+            _check_device(self._device, "grads")
+        if stream is not None and _stream_ptr(stream) != _stream_ptr(None):
+            if not isinstance(stream, torch.cuda.Stream):
+                ptr = _stream_ptr(stream)
+                stream = torch.cuda.ExternalStream(ptr) if ptr else torch.cuda.default_stream()
+            with torch.cuda.stream(stream):     # the allocations below belong to that stream
+                return self._call(fn, what, head, p, max_norm, eps, with_scale, None)
+        device = torch.device("cuda", torch.cuda.current_device() if self._device is None else self._device)
+        norm = torch.empty((), dtype=torch.float32, device=device)
+        scale = torch.empty((), dtype=torch.float32, device=device) if with_scale else None
+        work = torch.empty(self._bytes, dtype=torch.uint8, device=device)
+        code = fn(self._g, self._gt, self._numels, self._n, *head, float(p), float(max_norm), float(eps),
+                  norm.data_ptr(), None if scale is None else scale.data_ptr(), work.data_ptr(),
+                  self._bytes, _stream_ptr(None))
+        _check(code, what)
+        return (norm, scale) if with_scale else norm
+
+    def norm(self, norm_type: float = 2.0, stream=None) -> torch.Tensor:
+        """The norm over every gradient of the group, as a 0-d fp32 tensor.
+        ``norm_type``: 1, 2 or inf (the largest magnitude)."""
+        return self._call(library().muon_grad_norm, "muon_grad_norm", (), norm_type, float("inf"), 0.0,
+                          False, stream)
+
+    def clip_scale(self, max_norm: float, norm_type: float = 2.0, eps: float = 1e-6, stream=None):
+        """(norm, scale): the norm, and min(1, max_norm / (norm + eps)) to be
+        passed to the steps as ``grad_scale``.  Both 0-d fp32 tensors."""
+        return self._call(library().muon_grad_norm, "muon_grad_norm", (), norm_type, max_norm, eps,
+                          True, stream)
+
+    def clip(self, max_norm: float, norm_type: float = 2.0, eps: float = 1e-6, stream=None) -> torch.Tensor:
+        """Multiplies every gradient by min(1, max_norm / (norm + eps)), in
+        place or into ``out``, and returns the norm they had."""
+        if not self._clippable:
+            raise ValueError("tensors that clip writes must not overlap other tensors of the group")
+        return self._call(library().muon_clip_grads, "muon_clip_grads", (self._o, self._ot), norm_type,
+                          max_norm, eps, False, stream)
+
+
+def grad_norm(grads: Sequence[torch.Tensor], norm_type: float = 2.0, stream=None) -> torch.Tensor:
+    """The norm over every gradient of the list, as a 0-d fp32 tensor
+    (GradGroup.norm; a loop over the same tensors keeps a GradGroup)."""
+    return GradGroup(grads).norm(norm_type, stream)
+
+
+def clip_scale(grads: Sequence[torch.Tensor], max_norm: float, norm_type: float = 2.0,
+               eps: float = 1e-6, stream=None):
+    """(norm, scale) of the list, the scale for the steps' ``grad_scale``:
+    the steps then take clipped gradients without a pass that writes them."""
+    return GradGroup(grads).clip_scale(max_norm, norm_type, eps, stream)
+
+
+def clip_grads(grads: Sequence[torch.Tensor], max_norm: float, norm_type: float = 2.0,
+               eps: float = 1e-6, out: Sequence[torch.Tensor] | None = None, stream=None) -> torch.Tensor:
+    """Clip the list to ``max_norm``, in place or into ``out`` (same shapes,
+    any of the three types), and return the norm it had."""
+    return GradGroup(grads, out).clip(max_norm, norm_type, eps, stream)
 
 
 def orthogonalize(x: torch.Tensor, ns_steps: int = 5, coeffs=DEFAULT_COEFFS,
@@ -331,8 +496,9 @@ def _ld8(n: int) -> int:
     return (n + 7) // 8 * 8
 
 
-def momentum_normalize(grads, bufs, beta=0.95, nesterov=True, stream=None):
-    """The fused first kernel alone; returns oriented bf16 X0 views (m x n)."""
+def momentum_normalize(grads, bufs, beta=0.95, nesterov=True, stream=None, grad_scale=None):
+    """The fused first kernel alone; returns oriented bf16 X0 views (m x n).
+    ``grad_scale`` as for step."""
     n = len(grads)
     x0s, lds, shapes, outs = [], [], [], []
     for g, b in zip(grads, bufs):
@@ -346,10 +512,10 @@ def momentum_normalize(grads, bufs, beta=0.95, nesterov=True, stream=None):
         outs.append(x[:, :nn])
         lds.append(ld)
         shapes += [r, c]
-    code = library().muon_momentum_normalize(
+    code = library().muon_momentum_normalize_scaled(
         _ptr_array(grads), _ptr_array(bufs), _ptr_array(x0s), (ctypes.c_int64 * n)(*lds),
         (ctypes.c_int64 * len(shapes))(*shapes), n, float(beta), int(bool(nesterov)),
-        _stream_ptr(stream))
+        _scale_ptr(grad_scale), _stream_ptr(stream))
     _check(code, "muon_momentum_normalize")
     return outs
 

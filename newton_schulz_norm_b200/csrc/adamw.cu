@@ -30,15 +30,27 @@ __device__ __forceinline__ void adamw_elem(float& p, float g, float& m, float& v
   p = fmaf(p, decay, -(L.step_size * m) / den);              // decay, then the Adam move
 }
 
-__device__ __forceinline__ void scalar_elem(const AdamWTensor& T, long long e, const AdamWLaunch& L) {
+// The gradient the step takes: as stored, or (SCALED) times the scale, rounded
+// once to fp32, so that a scaled step gives exactly what scaling the gradients
+// in memory first would give.
+template <bool SCALED>
+__device__ __forceinline__ float taken(float g, float s) {
+  return SCALED ? __fmul_rn(s, g) : g;
+}
+
+template <bool SCALED>
+__device__ __forceinline__ void scalar_elem(const AdamWTensor& T, long long e, const AdamWLaunch& L,
+                                            float s) {
   float p = __ldcs(T.p + e), g = __ldcs(T.g + e), m = __ldcs(T.m + e), v = __ldcs(T.v + e);
-  adamw_elem(p, g, m, v, L, T.decay);
+  adamw_elem(p, taken<SCALED>(g, s), m, v, L, T.decay);
   __stcs(T.p + e, p);
   __stcs(T.m + e, m);
   __stcs(T.v + e, v);
 }
 
+template <bool SCALED>
 __global__ void __launch_bounds__(ADAMW_THREADS, 4) adamw_kernel(const __grid_constant__ AdamWLaunch L) {
+  const float s = SCALED ? __ldg(L.grad_scale) : 1.f;
   int ti = 0;
   for (int c = blockIdx.x; c < L.nchunks; c += gridDim.x) {
     while (ti + 1 < L.n && L.t[ti + 1].chunk0 <= c) ++ti;   // chunks only grow
@@ -66,10 +78,10 @@ __global__ void __launch_bounds__(ADAMW_THREADS, 4) adamw_kernel(const __grid_co
       for (int j = 0; j < ADAMW_VEC; ++j) {
         const long long q = q0 + threadIdx.x + (long long)j * ADAMW_THREADS;
         if (q < q1) {
-          adamw_elem(p[j].x, g[j].x, m[j].x, v[j].x, L, T.decay);
-          adamw_elem(p[j].y, g[j].y, m[j].y, v[j].y, L, T.decay);
-          adamw_elem(p[j].z, g[j].z, m[j].z, v[j].z, L, T.decay);
-          adamw_elem(p[j].w, g[j].w, m[j].w, v[j].w, L, T.decay);
+          adamw_elem(p[j].x, taken<SCALED>(g[j].x, s), m[j].x, v[j].x, L, T.decay);
+          adamw_elem(p[j].y, taken<SCALED>(g[j].y, s), m[j].y, v[j].y, L, T.decay);
+          adamw_elem(p[j].z, taken<SCALED>(g[j].z, s), m[j].z, v[j].z, L, T.decay);
+          adamw_elem(p[j].w, taken<SCALED>(g[j].w, s), m[j].w, v[j].w, L, T.decay);
           __stcs(reinterpret_cast<float4*>(T.p) + q, p[j]);
           __stcs(reinterpret_cast<float4*>(T.m) + q, m[j]);
           __stcs(reinterpret_cast<float4*>(T.v) + q, v[j]);
@@ -77,9 +89,9 @@ __global__ void __launch_bounds__(ADAMW_THREADS, 4) adamw_kernel(const __grid_co
       }
       // the last chunk of a tensor whose length is not a multiple of 4
       const long long e = (q1 << 2) + threadIdx.x;
-      if (e < e1) scalar_elem(T, e, L);
+      if (e < e1) scalar_elem<SCALED>(T, e, L, s);
     } else {
-      for (long long e = e0 + threadIdx.x; e < e1; e += ADAMW_THREADS) scalar_elem(T, e, L);
+      for (long long e = e0 + threadIdx.x; e < e1; e += ADAMW_THREADS) scalar_elem<SCALED>(T, e, L, s);
     }
   }
 }
@@ -88,7 +100,7 @@ __global__ void __launch_bounds__(ADAMW_THREADS, 4) adamw_kernel(const __grid_co
 
 int adamw_blocks_per_sm() {
   int n = 0;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, adamw_kernel, ADAMW_THREADS, 0) != cudaSuccess ||
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, adamw_kernel<false>, ADAMW_THREADS, 0) != cudaSuccess ||
       n < 1)
     return 1;
   return n;
@@ -96,7 +108,8 @@ int adamw_blocks_per_sm() {
 
 cudaError_t launch_adamw(const AdamWLaunch& L, int grid, cudaStream_t stream) {
   if (L.nchunks <= 0 || L.n <= 0) return cudaSuccess;
-  adamw_kernel<<<grid, ADAMW_THREADS, 0, stream>>>(L);
+  if (L.grad_scale) adamw_kernel<true><<<grid, ADAMW_THREADS, 0, stream>>>(L);
+  else adamw_kernel<false><<<grid, ADAMW_THREADS, 0, stream>>>(L);
   return cudaGetLastError();
 }
 

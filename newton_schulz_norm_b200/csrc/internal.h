@@ -181,6 +181,7 @@ struct K1Launch {
   int mode;
   int nesterov;
   float beta;
+  const float* grad_scale;   // device scalar that multiplies every gradient, or nullptr
   int* counter;              // work-queue head (zeroed before launch)
   int* done;                 // [n] pass-1 tiles finished (zeroed)
   int* ready;                // [n] norm published (zeroed)
@@ -230,7 +231,47 @@ struct AdamWLaunch {
   float step_size;           // fp32(lr / (1 - beta1^t))
   float inv_sqrt_bc2;        // fp32(1 / sqrt(1 - beta2^t))
   float eps;
+  const float* grad_scale;   // device scalar that multiplies every gradient, or nullptr
   AdamWTensor t[ADAMW_MAX_TENSORS];
+};
+
+// ---------------------------------------------------------------- gradient norm and clipping
+// Every tensor is cut into chunks of GRAD_CHUNK_VECS 16-byte vectors;
+// persistent CTAs take chunks in grid-stride order.
+constexpr int GRAD_THREADS = 256;
+constexpr int GRAD_VEC = 4;                                    // vectors per thread and chunk
+constexpr int GRAD_CHUNK_VECS = GRAD_THREADS * GRAD_VEC;       // 16 KB
+constexpr int GRAD_MAX_TENSORS = 512;                          // per launch
+constexpr int GRAD_MAX_CTAS = 148 * 8;                         // partial sums of one launch
+
+enum GradNorm : int { GRAD_L1 = 1, GRAD_L2 = 2, GRAD_INF = 3 };
+enum GradStage : int {
+  GRAD_STAGE_PARTIAL = 0,    // one partial sum per CTA
+  GRAD_STAGE_FINISH = 1,     // the norm and the scale from every partial sum
+  GRAD_STAGE_SCALE = 2,      // the same, and the gradients scaled
+};
+
+struct GradTensor {
+  const void* g;
+  void* out;                 // scaled gradients (may be g); unused for the norm alone
+  long long numel;           // > 0
+  int chunk0;                // first chunk of this tensor in the launch
+  unsigned char dtype;       // muon_dtype_t of g
+  unsigned char out_dtype;   // muon_dtype_t of out
+  unsigned char mis;         // elements of g past a 16-byte boundary
+  unsigned char out_vec;     // out is aligned for vector stores at g's vector starts
+};
+
+struct GradLaunch {
+  int n;                     // tensors in this launch
+  int nchunks;               // chunks of all of them
+  int part0;                 // first partial sum this launch writes
+  int npartials;             // partial sums of all launches of the call
+  unsigned long long* partials;
+  float* norm;
+  float* scale;
+  double max_norm, eps;
+  GradTensor t[GRAD_MAX_TENSORS];
 };
 
 // ---------------------------------------------------------------- launchers
@@ -244,6 +285,9 @@ int k1_blocks_per_sm();
 cudaError_t launch_apply(const ApplyLaunch& L, cudaStream_t stream);
 cudaError_t launch_adamw(const AdamWLaunch& L, int grid, cudaStream_t stream);
 int adamw_blocks_per_sm();
+int grad_blocks_per_sm();
+// norm: a GradNorm.
+cudaError_t launch_grad(const GradLaunch& L, int norm, GradStage stage, int grid, cudaStream_t stream);
 // The bound of every device-side wait, in ns (muon_set_wait_limit_ns, else
 // MUON_SPIN_LIMIT_NS at first use, else 2 s).  Takes the interface's lock.
 unsigned long long current_wait_limit_ns();

@@ -82,6 +82,14 @@ __device__ __forceinline__ double block_sum(double v, double* red) {
   return t;  // valid in thread 0 only
 }
 
+// The gradient the step takes: as stored, or (SCALED) times the launch's
+// device-side scale, rounded once to fp32.  Both passes form it the same way,
+// so the second one recomputes u exactly.
+template <bool SCALED>
+__device__ __forceinline__ float taken(float g, float s) {
+  return SCALED ? __fmul_rn(s, g) : g;
+}
+
 __device__ __forceinline__ float momentum_u(float g, float& b, float beta, int mode, int nesterov) {
   if (mode == K1_PLAIN) return g;
   b = fmaf(beta, b, g);
@@ -95,9 +103,10 @@ __device__ __forceinline__ float u_from(float g, float bnew, float beta, int mod
 
 // Pass 1 on one 64 x 64 tile: momentum (buf written back) and this thread's
 // sum of squares of u.  Every load of the thread is issued before any store.
+template <bool SCALED>
 __device__ __forceinline__ double pass1_tile(const K1Launch& L, const K1Ptrs& P, long long r,
                                              long long c, long long r0, long long c0, int lrow,
-                                             int lcol, uint64_t pol) {
+                                             int lcol, float s, uint64_t pol) {
   const bool vec = (c & 3) == 0;
   const float beta = L.beta;
   double ss = 0.0;
@@ -126,7 +135,7 @@ __device__ __forceinline__ double pass1_tile(const K1Launch& L, const K1Ptrs& P,
       float sq = 0.f;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float u = momentum_u(gv[e], bv[e], beta, L.mode, L.nesterov);
+        const float u = momentum_u(taken<SCALED>(gv[e], s), bv[e], beta, L.mode, L.nesterov);
         sq = fmaf(u, u, sq);
       }
       ss += (double)sq;
@@ -136,7 +145,7 @@ __device__ __forceinline__ double pass1_tile(const K1Launch& L, const K1Ptrs& P,
       const long long off = gr * c + gc;
       for (int e = 0; e < 4 && gc + e < c; ++e) {
         float b = (L.mode != K1_PLAIN) ? P.buf[off + e] : 0.f;
-        const float u = momentum_u(P.g[off + e], b, beta, L.mode, L.nesterov);
+        const float u = momentum_u(taken<SCALED>(P.g[off + e], s), b, beta, L.mode, L.nesterov);
         ss += (double)u * (double)u;
         if (L.mode != K1_PLAIN) P.buf[off + e] = b;
       }
@@ -147,10 +156,11 @@ __device__ __forceinline__ double pass1_tile(const K1Launch& L, const K1Ptrs& P,
 
 // Pass 2 on one 64 x 64 tile: recompute u from g and the new buf, scale by
 // 1/(norm + eps) in double, round once to bf16 and store oriented.
+template <bool SCALED>
 __device__ __forceinline__ void pass2_tile(const K1Launch& L, const K1Ptrs& P, const K1Info& info,
                                            long long r0, long long c0, double inv, int tid,
                                            int lrow, int lcol, uint16_t (*s_tile)[K1_TILE + 2],
-                                           uint64_t pol) {
+                                           float s, uint64_t pol) {
   const long long r = info.r, c = info.c;
   const bool vec = (c & 3) == 0;
   const float beta = L.beta;
@@ -183,13 +193,13 @@ __device__ __forceinline__ void pass2_tile(const K1Launch& L, const K1Ptrs& P, c
         const float bv[4] = {b4[k].x, b4[k].y, b4[k].z, b4[k].w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float u = u_from(gv[e], bv[e], beta, L.mode, L.nesterov);
+          const float u = u_from(taken<SCALED>(gv[e], s), bv[e], beta, L.mode, L.nesterov);
           bits[e] = __bfloat16_as_ushort(__double2bfloat16((double)u * inv));
         }
       } else {
         for (int e = 0; e < 4 && gc + e < c; ++e) {
           const float b = (L.mode != K1_PLAIN) ? __ldcg(P.buf + off + e) : 0.f;
-          const float u = u_from(P.g[off + e], b, beta, L.mode, L.nesterov);
+          const float u = u_from(taken<SCALED>(P.g[off + e], s), b, beta, L.mode, L.nesterov);
           bits[e] = __bfloat16_as_ushort(__double2bfloat16((double)u * inv));
         }
       }
@@ -236,6 +246,7 @@ __device__ __forceinline__ void pass2_tile(const K1Launch& L, const K1Ptrs& P, c
   }
 }
 
+template <bool SCALED>
 __global__ void __launch_bounds__(K1_THREADS, 4) k1_kernel(const __grid_constant__ K1Launch L) {
   __shared__ int s_item;
   __shared__ int s_flag;
@@ -244,6 +255,7 @@ __global__ void __launch_bounds__(K1_THREADS, 4) k1_kernel(const __grid_constant
   __shared__ uint16_t s_tile[K1_TILE][K1_TILE + 2];
 
   const int tid = threadIdx.x;
+  const float s = SCALED ? __ldg(L.grad_scale) : 1.f;
   const uint64_t pol_keep = policy_evict_last();
   const uint64_t pol_drop = policy_evict_first();
   const int lrow = tid >> 4;         // 0..15
@@ -282,7 +294,7 @@ __global__ void __launch_bounds__(K1_THREADS, 4) k1_kernel(const __grid_constant
       for (int t = t0; t < t1; ++t) {
         const long long r0 = (long long)(t / info.tiles_c) * K1_TILE;
         const long long c0 = (long long)(t % info.tiles_c) * K1_TILE;
-        ss += pass1_tile(L, P, info.r, info.c, r0, c0, lrow, lcol, pol_keep);
+        ss += pass1_tile<SCALED>(L, P, info.r, info.c, r0, c0, lrow, lcol, s, pol_keep);
       }
       const double tot = block_sum(ss, s_red);
       if (tid == 0) {
@@ -329,7 +341,7 @@ __global__ void __launch_bounds__(K1_THREADS, 4) k1_kernel(const __grid_constant
     for (int t = t0; t < t1; ++t) {
       const long long r0 = (long long)(t / info.tiles_c) * K1_TILE;
       const long long c0 = (long long)(t % info.tiles_c) * K1_TILE;
-      pass2_tile(L, P, info, r0, c0, inv, tid, lrow, lcol, s_tile, pol_drop);
+      pass2_tile<SCALED>(L, P, info, r0, c0, inv, tid, lrow, lcol, s_tile, s, pol_drop);
     }
   }
 }
@@ -361,14 +373,15 @@ __global__ void apply_kernel(const __grid_constant__ ApplyLaunch L) {
 
 int k1_blocks_per_sm() {
   int n = 0;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k1_kernel, K1_THREADS, 0) != cudaSuccess || n < 1)
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k1_kernel<false>, K1_THREADS, 0) != cudaSuccess || n < 1)
     return 1;
   return n;
 }
 
 cudaError_t launch_k1(const K1Launch& L, int grid, cudaStream_t stream) {
   if (L.nitems <= 0) return cudaSuccess;
-  k1_kernel<<<grid, K1_THREADS, 0, stream>>>(L);
+  if (L.grad_scale) k1_kernel<true><<<grid, K1_THREADS, 0, stream>>>(L);
+  else k1_kernel<false><<<grid, K1_THREADS, 0, stream>>>(L);
   return cudaGetLastError();
 }
 

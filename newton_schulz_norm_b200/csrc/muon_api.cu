@@ -16,6 +16,7 @@
 #include <map>
 #include <memory>
 #include <mutex>
+#include <new>
 #include <vector>
 
 #include <nvtx3/nvToolsExt.h>
@@ -199,6 +200,7 @@ struct DeviceCtx {
   int num_sms = 0;
   int k1_blocks_per_sm = 1;
   int adamw_blocks_per_sm = 1;
+  int grad_blocks_per_sm = 1;
   int max_pairs = 1;           // co-resident CTA pairs of the GEMM kernels
   int* status = nullptr;
   std::map<std::vector<long long>, std::unique_ptr<Plan>> plans;
@@ -210,7 +212,7 @@ std::map<int, std::unique_ptr<DeviceCtx>> g_ctx;
 // ---------------------------------------------------------------- profiling events
 enum ProfKind : int {
   PK_K1 = 0, PK_GRAM = 1, PK_POLY = 2, PK_UPDATE = 3, PK_FINAL = 4, PK_APPLY = 5, PK_ADAMW = 6,
-  PK_CHAIN = 7
+  PK_CHAIN = 7, PK_GRAD_NORM = 8, PK_GRAD_SCALE = 9
 };
 
 struct ProfRecord {
@@ -243,7 +245,8 @@ Profiler g_prof;
 const char* const kProfNames[] = {"muon: momentum/norm/cast", "muon: Gram",
                                   "muon: polynomial",         "muon: X update",
                                   "muon: final X update",     "muon: update (no NS)",
-                                  "muon: AdamW",              "muon: NS chain"};
+                                  "muon: AdamW",              "muon: NS chain",
+                                  "muon: gradient norm",      "muon: gradient scaling"};
 
 struct ProfScope {
   int kind;
@@ -290,6 +293,7 @@ int get_ctx(DeviceCtx** out) {
   if (ctx->max_pairs < 1) ctx->max_pairs = std::max(1, prop.multiProcessorCount / 2);
   ctx->k1_blocks_per_sm = k1_blocks_per_sm();   // persistent: as many CTAs as fit
   ctx->adamw_blocks_per_sm = adamw_blocks_per_sm();
+  ctx->grad_blocks_per_sm = grad_blocks_per_sm();
   *out = ctx.get();
   g_ctx[dev] = std::move(ctx);
   return MUON_OK;
@@ -676,7 +680,7 @@ int k1_grid(DeviceCtx* ctx, int nitems) {
 // zero_deps: how many chain counters after the K1 counters to zero as well
 // (the same memset), for the chain launch that follows.
 int run_k1(DeviceCtx* ctx, Plan* P, const K1Ptrs* ptrs, int mode, float beta, int nesterov,
-           cudaStream_t stream, int zero_deps = 0) {
+           const float* grad_scale, cudaStream_t stream, int zero_deps = 0) {
   const int n = P->k1.n;
   if (cudaMemsetAsync(P->k1.counters, 0, sizeof(int) * (1 + 2 * n + (size_t)zero_deps), stream) !=
       cudaSuccess)
@@ -690,6 +694,7 @@ int run_k1(DeviceCtx* ctx, Plan* P, const K1Ptrs* ptrs, int mode, float beta, in
   L.mode = mode;
   L.nesterov = nesterov;
   L.beta = beta;
+  L.grad_scale = grad_scale;
   L.counter = P->k1.counters;
   L.done = P->k1.counters + 1;
   L.ready = P->k1.counters + 1 + n;
@@ -943,8 +948,8 @@ int ensure_mirror_table(Plan* P, float* const* tab, int count, cudaStream_t stre
 
 int step_group(DeviceCtx* ctx, float* const* params, const float* const* grads, float* const* bufs,
                const int64_t* shapes, int n, float lr, float beta, int nesterov, int ns_steps,
-               const float* co, cudaStream_t stream, float* const* mirror_tab = nullptr,
-               int n_mirrors = 0) {
+               const float* co, const float* grad_scale, cudaStream_t stream,
+               float* const* mirror_tab = nullptr, int n_mirrors = 0) {
   std::vector<Geom> geom = make_geom(shapes, n);
   Plan* P = nullptr;
   int rc = get_plan(ctx, shape_key('S', geom), geom, true, &P);
@@ -959,7 +964,7 @@ int step_group(DeviceCtx* ctx, float* const* params, const float* const* grads, 
     const double s = std::sqrt(std::max(1.0, (double)geom[i].r / (double)geom[i].c));
     F.scale[i] = (float)((double)lr * s);
   }
-  rc = run_k1(ctx, P, ptrs.data(), K1_MOMENTUM, beta, nesterov, stream,
+  rc = run_k1(ctx, P, ptrs.data(), K1_MOMENTUM, beta, nesterov, grad_scale, stream,
               chain_deps(ctx, P, ns_steps));
   if (rc) return rc;
   if (ns_steps == 0) {
@@ -978,6 +983,141 @@ int step_group(DeviceCtx* ctx, float* const* params, const float* const* grads, 
   return run_ns(ctx, P, ns_steps, co, FINAL_PARAM, &F, stream, pmaps, mirrors, n_mirrors);
 }
 
+// Runs an entry point's body; no C++ exception leaves it.
+template <class F>
+int guarded(F body) {
+  try {
+    return body();
+  } catch (const std::bad_alloc&) {
+    return MUON_ERR_NOMEM;
+  } catch (...) {
+    return MUON_ERR_CUDA;
+  }
+}
+
+// A device-side gradient scale: NULL (none) or the address of one float.
+bool scale_ok(const float* grad_scale) { return (reinterpret_cast<uintptr_t>(grad_scale) & 3u) == 0; }
+
+// ---------------------------------------------------------------- gradient norm and clipping
+
+constexpr long long kGradMaxNumel = (1ll << 40);
+constexpr long long kGradMaxChunks = (1ll << 30);   // of one launch
+
+int dtype_size(int dtype) { return dtype == MUON_F32 ? 4 : 2; }
+
+// Chunks of one tensor; a tensor that starts off a 16-byte boundary may touch
+// one vector more than its length alone would.
+long long grad_chunks(long long numel, int mis, int dtype) {
+  return cdiv(cdiv(numel + mis, 16 / dtype_size(dtype)), GRAD_CHUNK_VECS);
+}
+
+int grad_norm_of(double p) {
+  if (p == 1.0) return GRAD_L1;
+  if (p == 2.0) return GRAD_L2;
+  if (std::isinf(p) && p > 0) return GRAD_INF;
+  return 0;
+}
+
+// The number of launches that n tensors take: a launch ends when its table or
+// its chunk count is full.  The alignment is not known here, so every tensor
+// counts the vector that a bad alignment can add.
+long long grad_launches(const unsigned char* dtypes, const int64_t* numels, int n) {
+  long long launches = 0, chunks = 0;
+  int held = 0;
+  for (int i = 0; i < n; ++i) {
+    if (numels[i] == 0) continue;
+    const long long c = grad_chunks(numels[i], 16 / dtype_size(dtypes[i]) - 1, dtypes[i]);
+    if (launches == 0 || held == GRAD_MAX_TENSORS || chunks + c > kGradMaxChunks) {
+      ++launches;
+      held = 0;
+      chunks = 0;
+    }
+    ++held;
+    chunks += c;
+  }
+  return launches;
+}
+
+int check_grad_list(const void* const* ptrs, const unsigned char* dtypes, const int64_t* numels, int n) {
+  if (n > 0 && (!ptrs || !dtypes || !numels)) return MUON_ERR_INVALID_ARG;
+  for (int i = 0; i < n; ++i) {
+    if (numels[i] < 0 || numels[i] > kGradMaxNumel || dtypes[i] > MUON_F16) return MUON_ERR_INVALID_ARG;
+    if (numels[i] == 0) continue;
+    if (!ptrs[i]) return MUON_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(ptrs[i]) % dtype_size(dtypes[i])) return MUON_ERR_UNSUPPORTED;
+  }
+  return MUON_OK;
+}
+
+// The launches of a norm (outs == nullptr) or of a clip.
+int run_grad(const void* const* grads, const unsigned char* dtypes, const int64_t* numels, int n,
+             void* const* outs, const unsigned char* out_dtypes, int norm_kind, double max_norm,
+             double eps, float* norm, float* scale, void* workspace, cudaStream_t stream) {
+  std::lock_guard<std::mutex> lock(g_mutex);
+  DeviceCtx* ctx = nullptr;
+  int rc = get_ctx(&ctx);
+  if (rc) return rc;
+  const int max_grid = std::min(GRAD_MAX_CTAS, ctx->num_sms * ctx->grad_blocks_per_sm);
+  static thread_local GradLaunch L;
+  L.partials = static_cast<unsigned long long*>(workspace);
+  L.max_norm = max_norm;
+  L.eps = eps;
+  L.npartials = 0;
+  // Walks the tensors launch by launch.  The scaling launches come after all
+  // of the norm's, so the tables are built a second time for them.
+  auto walk = [&](GradStage stage, float* out_norm, float* out_scale) -> int {
+    L.norm = out_norm;
+    L.scale = out_scale;
+    L.n = 0;
+    L.nchunks = 0;
+    auto flush = [&]() -> int {
+      if (L.n == 0) return MUON_OK;
+      const int grid = std::max(1, std::min(L.nchunks, max_grid));
+      if (stage == GRAD_STAGE_PARTIAL) {
+        L.part0 = L.npartials;
+        L.npartials += grid;
+      }
+      ProfScope ps(stage == GRAD_STAGE_PARTIAL ? PK_GRAD_NORM : PK_GRAD_SCALE, stream);
+      const int r = cuda_err(launch_grad(L, norm_kind, stage, grid, stream));
+      L.norm = nullptr;    // written by the first scaling launch
+      L.scale = nullptr;
+      L.n = 0;
+      L.nchunks = 0;
+      return r;
+    };
+    for (int i = 0; i < n; ++i) {
+      if (numels[i] == 0) continue;
+      const int size = dtype_size(dtypes[i]), E = 16 / size;
+      const int mis = (int)((reinterpret_cast<uintptr_t>(grads[i]) & 15u) / size);
+      const long long chunks = grad_chunks(numels[i], mis, dtypes[i]);
+      if (L.n == GRAD_MAX_TENSORS || L.nchunks + chunks > kGradMaxChunks) {
+        const int r = flush();
+        if (r) return r;
+      }
+      GradTensor& T = L.t[L.n++];
+      T.g = grads[i];
+      T.out = outs ? outs[i] : nullptr;
+      T.numel = numels[i];
+      T.chunk0 = L.nchunks;
+      T.dtype = dtypes[i];
+      T.out_dtype = outs ? out_dtypes[i] : dtypes[i];
+      T.mis = (unsigned char)mis;
+      const int out_size = dtype_size(T.out_dtype);
+      T.out_vec = (reinterpret_cast<uintptr_t>(T.out) - (uintptr_t)(mis * out_size)) %
+                      std::min(16, E * out_size) == 0;
+      L.nchunks += (int)chunks;
+    }
+    return flush();
+  };
+  rc = walk(GRAD_STAGE_PARTIAL, nullptr, nullptr);
+  if (rc) return rc;
+  if (outs && L.npartials > 0) return walk(GRAD_STAGE_SCALE, norm, scale);
+  L.norm = norm;
+  L.scale = scale;
+  ProfScope ps(PK_GRAD_NORM, stream);
+  return cuda_err(launch_grad(L, norm_kind, GRAD_STAGE_FINISH, 1, stream));
+}
+
 }  // namespace
 
 unsigned long long current_wait_limit_ns() {
@@ -991,12 +1131,13 @@ using namespace muon;
 
 extern "C" {
 
-int muon_step_mirrored(float* const* params, const float* const* grads, float* const* bufs,
-                       const int64_t* shapes, int n, float lr, float beta, int nesterov,
-                       int ns_steps, const float* coeffs, float* const* mirrors, int n_mirrors,
-                       void* stream) {
+int muon_step_scaled(float* const* params, const float* const* grads, float* const* bufs,
+                     const int64_t* shapes, int n, float lr, float beta, int nesterov, int ns_steps,
+                     const float* coeffs, float* const* mirrors, int n_mirrors,
+                     const float* grad_scale, void* stream) {
   int rc = check_shapes(shapes, n);
   if (rc) return rc;
+  if (!scale_ok(grad_scale)) return MUON_ERR_UNSUPPORTED;
   if (n_mirrors < 0 || n_mirrors > MUON_MAX_MIRRORS) return MUON_ERR_INVALID_ARG;
   if (n == 0) return MUON_OK;
   if (!params || !grads || !bufs) return MUON_ERR_INVALID_ARG;
@@ -1033,24 +1174,34 @@ int muon_step_mirrored(float* const* params, const float* const* grads, float* c
     for (int k = 0; k < n_mirrors; ++k)
       for (int i = 0; i < gn; ++i) tab[(size_t)k * gn + i] = mirrors[(size_t)k * n + g0 + i];
     rc = step_group(ctx, params + g0, grads + g0, bufs + g0, shapes + 2 * g0, gn, lr, beta, nesterov,
-                    ns_steps, co, static_cast<cudaStream_t>(stream), tab.data(), n_mirrors);
+                    ns_steps, co, grad_scale, static_cast<cudaStream_t>(stream), tab.data(), n_mirrors);
     if (rc) return rc;
   }
   return MUON_OK;
 }
 
+int muon_step_mirrored(float* const* params, const float* const* grads, float* const* bufs,
+                       const int64_t* shapes, int n, float lr, float beta, int nesterov,
+                       int ns_steps, const float* coeffs, float* const* mirrors, int n_mirrors,
+                       void* stream) {
+  return muon_step_scaled(params, grads, bufs, shapes, n, lr, beta, nesterov, ns_steps, coeffs, mirrors,
+                          n_mirrors, nullptr, stream);
+}
+
 int muon_step(float* const* params, const float* const* grads, float* const* bufs,
               const int64_t* shapes, int n, float lr, float beta, int nesterov, int ns_steps,
               const float* coeffs, void* stream) {
-  return muon_step_mirrored(params, grads, bufs, shapes, n, lr, beta, nesterov, ns_steps, coeffs,
-                            nullptr, 0, stream);
+  return muon_step_scaled(params, grads, bufs, shapes, n, lr, beta, nesterov, ns_steps, coeffs, nullptr, 0,
+                          nullptr, stream);
 }
 
-int muon_adamw_step(float* const* params, const float* const* grads, float* const* exp_avgs,
-                    float* const* exp_avg_sqs, const int64_t* numels, const unsigned char* decay,
-                    int n, int64_t step, double lr, double beta1, double beta2, double eps,
-                    double weight_decay, void* stream) {
+int muon_adamw_step_scaled(float* const* params, const float* const* grads, float* const* exp_avgs,
+                           float* const* exp_avg_sqs, const int64_t* numels,
+                           const unsigned char* decay, int n, int64_t step, double lr, double beta1,
+                           double beta2, double eps, double weight_decay, const float* grad_scale,
+                           void* stream) {
   if (n < 0) return MUON_ERR_INVALID_ARG;
+  if (!scale_ok(grad_scale)) return MUON_ERR_UNSUPPORTED;
   if (n == 0) return MUON_OK;
   if (!params || !grads || !exp_avgs || !exp_avg_sqs || !numels) return MUON_ERR_INVALID_ARG;
   if (step < 1) return MUON_ERR_INVALID_ARG;
@@ -1081,6 +1232,7 @@ int muon_adamw_step(float* const* params, const float* const* grads, float* cons
   L.step_size = (float)(lr / bc1);
   L.inv_sqrt_bc2 = (float)(1.0 / std::sqrt(bc2));
   L.eps = (float)eps;
+  L.grad_scale = grad_scale;
 
   std::lock_guard<std::mutex> lock(g_mutex);
   DeviceCtx* ctx = nullptr;
@@ -1123,6 +1275,52 @@ int muon_adamw_step(float* const* params, const float* const* grads, float* cons
   return flush();
 }
 
+int muon_adamw_step(float* const* params, const float* const* grads, float* const* exp_avgs,
+                    float* const* exp_avg_sqs, const int64_t* numels, const unsigned char* decay,
+                    int n, int64_t step, double lr, double beta1, double beta2, double eps,
+                    double weight_decay, void* stream) {
+  return muon_adamw_step_scaled(params, grads, exp_avgs, exp_avg_sqs, numels, decay, n, step, lr, beta1,
+                                beta2, eps, weight_decay, nullptr, stream);
+}
+
+int64_t muon_grad_workspace_bytes(const unsigned char* dtypes, const int64_t* numels, int n) {
+  if (n < 0 || (n > 0 && (!dtypes || !numels))) return -1;
+  for (int i = 0; i < n; ++i)
+    if (numels[i] < 0 || numels[i] > kGradMaxNumel || dtypes[i] > MUON_F16) return -1;
+  return std::max(1ll, grad_launches(dtypes, numels, n)) * GRAD_MAX_CTAS * 8;
+}
+
+int muon_grad_norm(const void* const* grads, const unsigned char* dtypes, const int64_t* numels, int n,
+                   double p, double max_norm, double eps, float* norm, float* scale, void* workspace,
+                   int64_t workspace_bytes, void* stream) {
+  return muon_clip_grads(grads, dtypes, numels, n, nullptr, nullptr, p, max_norm, eps, norm, scale,
+                         workspace, workspace_bytes, stream);
+}
+
+int muon_clip_grads(const void* const* grads, const unsigned char* dtypes, const int64_t* numels, int n,
+                    void* const* outs, const unsigned char* out_dtypes, double p, double max_norm,
+                    double eps, float* norm, float* scale, void* workspace, int64_t workspace_bytes,
+                    void* stream) {
+  if (n < 0 || !norm || !workspace) return MUON_ERR_INVALID_ARG;
+  const int kind = grad_norm_of(p);
+  if (kind == 0 || std::isnan(max_norm) || max_norm < 0 || !std::isfinite(eps) || eps < 0)
+    return MUON_ERR_INVALID_ARG;
+  int rc = check_grad_list(grads, dtypes, numels, n);
+  if (rc) return rc;
+  if (outs) {
+    rc = check_grad_list(outs, out_dtypes, numels, n);
+    if (rc) return rc;
+  }
+  if ((reinterpret_cast<uintptr_t>(norm) & 3u) || !scale_ok(scale) ||
+      (reinterpret_cast<uintptr_t>(workspace) & 7u))
+    return MUON_ERR_UNSUPPORTED;
+  if (workspace_bytes < muon_grad_workspace_bytes(dtypes, numels, n)) return MUON_ERR_INVALID_ARG;
+  return guarded([&] {
+    return run_grad(grads, dtypes, numels, n, outs, out_dtypes, kind, max_norm, eps, norm, scale,
+                    workspace, static_cast<cudaStream_t>(stream));
+  });
+}
+
 int muon_orthogonalize(const float* x, void* out, int out_is_bf16, int64_t rows, int64_t cols,
                        int ns_steps, const float* coeffs, void* stream) {
   const int64_t shp[2] = {rows, cols};
@@ -1147,7 +1345,7 @@ int muon_orthogonalize(const float* x, void* out, int out_is_bf16, int64_t rows,
   p.buf = nullptr;
   p.x0 = P->X[0];
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  rc = run_k1(ctx, P, &p, K1_PLAIN, 0.f, 0, s, chain_deps(ctx, P, ns_steps));
+  rc = run_k1(ctx, P, &p, K1_PLAIN, 0.f, 0, nullptr, s, chain_deps(ctx, P, ns_steps));
   if (rc) return rc;
   const int mode = out_is_bf16 ? FINAL_OUT_BF16 : FINAL_OUT_F32;
   if (ns_steps == 0) {
@@ -1163,8 +1361,15 @@ int muon_orthogonalize(const float* x, void* out, int out_is_bf16, int64_t rows,
 int muon_momentum_normalize(const float* const* grads, float* const* bufs, uint16_t* const* x0,
                             const int64_t* x0_ld, const int64_t* shapes, int n, float beta,
                             int nesterov, void* stream) {
+  return muon_momentum_normalize_scaled(grads, bufs, x0, x0_ld, shapes, n, beta, nesterov, nullptr, stream);
+}
+
+int muon_momentum_normalize_scaled(const float* const* grads, float* const* bufs, uint16_t* const* x0,
+                                   const int64_t* x0_ld, const int64_t* shapes, int n, float beta,
+                                   int nesterov, const float* grad_scale, void* stream) {
   int rc = check_shapes(shapes, n);
   if (rc) return rc;
+  if (!scale_ok(grad_scale)) return MUON_ERR_UNSUPPORTED;
   if (n == 0) return MUON_OK;
   if (n > MUON_MAX_GROUP) return MUON_ERR_INVALID_ARG;
   if (!grads || !bufs || !x0 || !x0_ld || !std::isfinite(beta)) return MUON_ERR_INVALID_ARG;
@@ -1193,7 +1398,8 @@ int muon_momentum_normalize(const float* const* grads, float* const* bufs, uint1
     ptrs[i].buf = bufs[i];
     ptrs[i].x0 = reinterpret_cast<__nv_bfloat16*>(x0[i]);
   }
-  return run_k1(ctx, P, ptrs.data(), K1_MOMENTUM, beta, nesterov, static_cast<cudaStream_t>(stream));
+  return run_k1(ctx, P, ptrs.data(), K1_MOMENTUM, beta, nesterov, grad_scale,
+                static_cast<cudaStream_t>(stream));
 }
 
 // One GEMM phase on caller buffers (stage entry points).

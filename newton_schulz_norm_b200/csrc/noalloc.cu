@@ -214,6 +214,7 @@ extern "C" int muon_momentum_normalize_noalloc(const float* const* grads, float*
   L.mode = K1_MOMENTUM;
   L.nesterov = nesterov;
   L.beta = beta;
+  L.grad_scale = nullptr;
   L.counter = scr->counters;
   L.done = scr->counters + 1;
   L.ready = scr->counters + 1 + n;

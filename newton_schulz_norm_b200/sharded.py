@@ -138,7 +138,7 @@ class ShardedMuon:
         return self.flat[k * self.seg:(k + 1) * self.seg]
 
     def step(self, grads: Sequence[torch.Tensor], lr: float, beta: float = 0.95,
-             nesterov: bool = True, coeffs=None, stream=None) -> None:
+             nesterov: bool = True, coeffs=None, stream=None, grad_scale=None) -> None:
         """One step.  ``stream`` (default: torch's current stream) runs the
         owned matrices' kernels, after everything already queued on torch's
         current stream (the previous step's exchange included).  The
@@ -147,7 +147,10 @@ class ShardedMuon:
         first, so it never reads parameters the kernels have not written
         yet.  In the fused mode every rank's kernels also wait for a device
         barrier at entry: no rank stores into another rank's copy while that
-        rank may still be reading its parameters from before this step."""
+        rank may still be reading its parameters from before this step.
+        ``grad_scale`` (optional: one fp32 CUDA element, the same on every
+        rank, as clip_scale over the full list gives it) multiplies every
+        gradient on the way into the owned matrices' kernels."""
         if len(grads) != len(self.shapes):
             raise ValueError("one gradient per matrix is required")
         cur = torch.cuda.current_stream() if self.flat.is_cuda else None
@@ -162,6 +165,8 @@ class ShardedMuon:
                 kw["coeffs"] = coeffs
             if stream is not None:
                 kw["stream"] = stream
+            if grad_scale is not None:
+                kw["grad_scale"] = grad_scale
             if self.fused:
                 kw["mirrors"] = self._mirrors
             self.step_fn([self.params[i] for i in self.owned], [grads[i] for i in self.owned],
