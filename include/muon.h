@@ -265,8 +265,8 @@ MUON_API int muon_adamw_step(float* const* params, const float* const* grads,
  *   norm    device float (4-byte aligned): N, rounded once to fp32.
  *   scale   device float or NULL: s, formed in fp64 and rounded once.
  *   workspace  device memory, 8-byte aligned, of at least
- *           muon_grad_workspace_bytes() bytes; needs no initialisation and
- *           holds nothing after the call.  Calls whose executions may overlap
+ *           muon_grad_workspace_bytes() bytes (NULL where that is 0); needs no
+ *           initialisation and holds nothing after the call.  Calls whose executions may overlap
  *           on the GPU (other streams, other graphs) need workspaces and
  *           results of their own; the library shares nothing between them.
  *   stream  cudaStream_t as void*.
@@ -281,7 +281,7 @@ MUON_API int muon_adamw_step(float* const* params, const float* const* grads,
 typedef enum { MUON_F32 = 0, MUON_BF16 = 1, MUON_F16 = 2 } muon_dtype_t;
 
 /* muon_grad_workspace_bytes -- workspace of the two calls below for these
- * tensors (host-only computation; -1 on a bad argument). */
+ * tensors, 0 for short lists (host-only computation; -1 on a bad argument). */
 MUON_API int64_t muon_grad_workspace_bytes(const unsigned char* dtypes, const int64_t* numels, int n);
 
 /* muon_grad_norm -- N and s; the gradients are only read. */

@@ -105,8 +105,15 @@ def _check(code: int, what: str):
         raise MuonError(code, what)
 
 
+# The current stream's handle without building a Stream object (0.1 instead of
+# 3.2 us per call), where this torch has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream_ptr(stream) -> int:
     if stream is None:
+        if _raw_stream is not None and torch.cuda.is_initialized():
+            return _raw_stream(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -347,6 +354,7 @@ def adamw_step_raw(param_ptrs, grad_ptrs, avg_ptrs, sq_ptrs, numels, step, lr, b
         int(stream) if stream is not None else None)
 
 
+_INF = float("inf")
 _DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
 
 
@@ -395,6 +403,9 @@ class GradGroup:
         if self._bytes < 0:
             raise ValueError("a gradient is too large")
         self._clippable = self._disjoint(grads, grads if out is None else out)
+        if self._device is None:
+            self._device = torch.cuda.current_device()
+        self._like = torch.empty(1, dtype=torch.float32, device=torch.device("cuda", self._device))
 
     @staticmethod
     def _disjoint(grads, outs) -> bool:
@@ -416,44 +427,41 @@ class GradGroup:
             ends[written] = max(ends[written], e)
         return True
 
-    def _call(self, fn, what, head, p, max_norm, eps, with_scale, stream):
-        if self._device is not None:
-            _check_device(self._device, "grads")
+    def _call(self, clip, p, max_norm, eps, with_scale, stream):
+        _check_device(self._device, "grads")
         if stream is not None and _stream_ptr(stream) != _stream_ptr(None):
             if not isinstance(stream, torch.cuda.Stream):
                 ptr = _stream_ptr(stream)
                 stream = torch.cuda.ExternalStream(ptr) if ptr else torch.cuda.default_stream()
             with torch.cuda.stream(stream):     # the allocations below belong to that stream
-                return self._call(fn, what, head, p, max_norm, eps, with_scale, None)
-        device = torch.device("cuda", torch.cuda.current_device() if self._device is None else self._device)
-        norm = torch.empty((), dtype=torch.float32, device=device)
-        scale = torch.empty((), dtype=torch.float32, device=device) if with_scale else None
-        work = torch.empty(self._bytes, dtype=torch.uint8, device=device)
-        code = fn(self._g, self._gt, self._numels, self._n, *head, float(p), float(max_norm), float(eps),
-                  norm.data_ptr(), None if scale is None else scale.data_ptr(), work.data_ptr(),
-                  self._bytes, _stream_ptr(None))
-        _check(code, what)
+                return self._call(clip, p, max_norm, eps, with_scale, None)
+        norm = self._like.new_empty(())
+        scale = self._like.new_empty(()) if with_scale else None
+        work = self._like.new_empty(self._bytes // 4) if self._bytes else None
+        code = library().muon_clip_grads(
+            self._g, self._gt, self._numels, self._n, self._o if clip else None,
+            self._ot if clip else None, p, max_norm, eps, norm.data_ptr(),
+            None if scale is None else scale.data_ptr(), None if work is None else work.data_ptr(),
+            self._bytes, _stream_ptr(None))
+        _check(code, "muon_clip_grads" if clip else "muon_grad_norm")
         return (norm, scale) if with_scale else norm
 
     def norm(self, norm_type: float = 2.0, stream=None) -> torch.Tensor:
         """The norm over every gradient of the group, as a 0-d fp32 tensor.
         ``norm_type``: 1, 2 or inf (the largest magnitude)."""
-        return self._call(library().muon_grad_norm, "muon_grad_norm", (), norm_type, float("inf"), 0.0,
-                          False, stream)
+        return self._call(False, norm_type, _INF, 0.0, False, stream)
 
     def clip_scale(self, max_norm: float, norm_type: float = 2.0, eps: float = 1e-6, stream=None):
         """(norm, scale): the norm, and min(1, max_norm / (norm + eps)) to be
         passed to the steps as ``grad_scale``.  Both 0-d fp32 tensors."""
-        return self._call(library().muon_grad_norm, "muon_grad_norm", (), norm_type, max_norm, eps,
-                          True, stream)
+        return self._call(False, norm_type, max_norm, eps, True, stream)
 
     def clip(self, max_norm: float, norm_type: float = 2.0, eps: float = 1e-6, stream=None) -> torch.Tensor:
         """Multiplies every gradient by min(1, max_norm / (norm + eps)), in
         place or into ``out``, and returns the norm they had."""
         if not self._clippable:
             raise ValueError("tensors that clip writes must not overlap other tensors of the group")
-        return self._call(library().muon_clip_grads, "muon_clip_grads", (self._o, self._ot), norm_type,
-                          max_norm, eps, False, stream)
+        return self._call(True, norm_type, max_norm, eps, False, stream)
 
 
 def grad_norm(grads: Sequence[torch.Tensor], norm_type: float = 2.0, stream=None) -> torch.Tensor:

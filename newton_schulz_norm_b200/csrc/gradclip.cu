@@ -5,12 +5,17 @@
 //   s = min(1, max_norm / (N + eps))
 //   out_i[e] = round(fp32(s * g_i[e]))      in place or into other tensors
 //
-// Two launches: grad_partial_kernel reads every gradient once and leaves one
-// partial sum per CTA in the caller's workspace; the second launch sums the
-// partials, each of its CTAs for itself and in one fixed order, and either
-// writes N and s (grad_finish_kernel) or scales the gradients
-// (grad_scale_kernel).  Nothing is counted or accumulated with atomics: the
-// same call on the same device gives the same bits.
+// Two forms, by the size of the list.  grad_cluster_kernel does all of it in
+// one launch of one thread-block cluster, whose CTAs exchange their partial
+// values through distributed shared memory.  Longer lists take two launches:
+// grad_partial_kernel reads every gradient once and leaves one partial value
+// per CTA in the caller's workspace; the second launch joins the partials,
+// each of its CTAs for itself and in one fixed order, and either writes N and
+// s (grad_finish_kernel) or scales the gradients (grad_scale_kernel).  The
+// second launch is a programmatic dependent of the first: its CTAs are
+// resident and waiting when the last partial value is written.  Nothing is
+// counted or accumulated with atomics, and no workspace outlives the call:
+// the same call on the same device gives the same bits, whatever runs beside.
 //
 // The squares are formed and summed in fp64.  In fp32 a square underflows
 // below |g| ~ 1e-19 and overflows above 1.8e19; in fp64 neither happens for
@@ -20,7 +25,10 @@
 // NaN above infinity, so a NaN is never lost.
 #include "internal.h"
 
+#include <cooperative_groups.h>
 #include <cuda_fp16.h>
+
+namespace cg = cooperative_groups;
 
 namespace muon {
 namespace {
@@ -55,6 +63,10 @@ struct Elem<MUON_BF16> {
   }
   static __device__ __forceinline__ float widen(__nv_bfloat16 x) { return __bfloat162float(x); }
   static __device__ __forceinline__ __nv_bfloat16 narrow(float x) { return __float2bfloat16_rn(x); }
+  static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
 };
 template <>
 struct Elem<MUON_F16> {
@@ -71,6 +83,10 @@ struct Elem<MUON_F16> {
   }
   static __device__ __forceinline__ float widen(__half x) { return __half2float(x); }
   static __device__ __forceinline__ __half narrow(float x) { return __float2half_rn(x); }
+  static __device__ __forceinline__ uint32_t pack(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
 };
 
 // ---------------------------------------------------------------- sums
@@ -109,8 +125,8 @@ struct Acc<GRAD_INF> {
   __device__ __forceinline__ double norm() const { return (double)__uint_as_float(v); }
 };
 
-// Joins the CTA's values in a fixed order; every thread gets the result.
-template <int P>
+// Joins the values of THREADS threads in a fixed order; every thread gets the result.
+template <int P, int THREADS>
 __device__ __forceinline__ Acc<P> block_join(Acc<P> a, unsigned long long* red) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) a.join(a.shuffled(o));
@@ -118,7 +134,7 @@ __device__ __forceinline__ Acc<P> block_join(Acc<P> a, unsigned long long* red) 
   __syncthreads();
   Acc<P> t;
 #pragma unroll
-  for (int w = 0; w < GRAD_THREADS / 32; ++w) {
+  for (int w = 0; w < THREADS / 32; ++w) {
     Acc<P> x;
     x.set(red[w]);
     t.join(x);
@@ -132,188 +148,324 @@ __device__ __forceinline__ Acc<P> block_join(Acc<P> a, unsigned long long* red) 
 // walked in the aligned vectors that cover it: vector v holds elements
 // [v E - mis, (v + 1) E - mis).  Only the first and the last can be partial;
 // those are read element by element, so nothing outside the tensor is touched.
+
+// The tensor that holds chunk c, from lo on: chunk0 ascends.
+__device__ __forceinline__ int tensor_of(const int* chunk0, int n, int c, int lo) {
+  int hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (chunk0[mid] <= c) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
 template <int P, int DT>
-__device__ __forceinline__ void partial_chunk(const GradTensor& T, long long v0, Acc<P>& acc) {
+__device__ __forceinline__ void norm_chunk(const GradTensor& T, long long v0, int tid, Acc<P>& acc) {
   typedef Elem<DT> X;
   constexpr int E = X::E;
-  const typename X::T* g = reinterpret_cast<const typename X::T*>(T.g);
-  const long long nvec = (T.numel + T.mis + E - 1) / E;
-  uint4 raw[GRAD_VEC];
-  bool full[GRAD_VEC];
+  const typename X::T* g = reinterpret_cast<const typename X::T*>(T.g) - T.mis;   // of vector 0
+  if ((v0 > 0 || T.mis == 0) && (v0 + GRAD_CHUNK_VECS) * E <= T.numel + T.mis) {
+    const uint4* p = reinterpret_cast<const uint4*>(g) + v0 + tid;
+    uint4 raw[GRAD_VEC];
 #pragma unroll
-  for (int j = 0; j < GRAD_VEC; ++j) {
-    const long long v = v0 + threadIdx.x + j * GRAD_THREADS;
-    const long long e = v * E - T.mis;
-    full[j] = e >= 0 && e + E <= T.numel;
-    raw[j] = make_uint4(0, 0, 0, 0);
-    if (full[j]) raw[j] = __ldg(reinterpret_cast<const uint4*>(g + e));
-  }
+    for (int j = 0; j < GRAD_VEC; ++j) raw[j] = __ldg(p + j * GRAD_THREADS);
 #pragma unroll
-  for (int j = 0; j < GRAD_VEC; ++j) {
-    const long long v = v0 + threadIdx.x + j * GRAD_THREADS;
-    if (full[j]) {
+    for (int j = 0; j < GRAD_VEC; ++j) {
       float f[E];
       X::unpack(raw[j], f);
 #pragma unroll
       for (int k = 0; k < E; ++k) acc.add(f[k]);
-    } else if (v < nvec) {
-      const long long e = v * E - T.mis;
+    }
+    return;
+  }
+  const long long end = T.numel + T.mis;   // elements are counted from vector 0 here
+  const long long v1 = min(v0 + GRAD_CHUNK_VECS, (end + E - 1) / E);
+  for (long long v = v0 + tid; v < v1; v += GRAD_THREADS) {
+    const long long e = v * E;
+    if (e >= T.mis && e + E <= end) {
+      float f[E];
+      X::unpack(__ldg(reinterpret_cast<const uint4*>(g) + v), f);
+#pragma unroll
+      for (int k = 0; k < E; ++k) acc.add(f[k]);
+    } else {
       for (int k = 0; k < E; ++k)
-        if (e + k >= 0 && e + k < T.numel) acc.add(X::widen(g[e + k]));
+        if (e + k >= T.mis && e + k < end) acc.add(X::widen(g[e + k]));
     }
   }
 }
 
 template <int P>
-__global__ void __launch_bounds__(GRAD_THREADS) grad_partial_kernel(const __grid_constant__ GradLaunch L) {
+__device__ __forceinline__ void norm_chunk_of(const GradTensor& T, long long v0, int tid, Acc<P>& acc) {
+  if (T.dtype == MUON_F32) norm_chunk<P, MUON_F32>(T, v0, tid, acc);
+  else if (T.dtype == MUON_BF16) norm_chunk<P, MUON_BF16>(T, v0, tid, acc);
+  else norm_chunk<P, MUON_F16>(T, v0, tid, acc);
+}
+
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+template <int P, int N>
+__global__ void __launch_bounds__(GRAD_THREADS, 4)
+    grad_partial_kernel(const __grid_constant__ GradLaunch<N> L) {
   __shared__ unsigned long long red[GRAD_THREADS / 32];
+  pdl_launch();
   Acc<P> acc;
   int ti = 0;
   for (int c = blockIdx.x; c < L.nchunks; c += gridDim.x) {
-    while (ti + 1 < L.n && L.t[ti + 1].chunk0 <= c) ++ti;   // chunks only grow
-    const GradTensor& T = L.t[ti];
-    const long long v0 = (long long)(c - T.chunk0) * GRAD_CHUNK_VECS;
-    if (T.dtype == MUON_F32) partial_chunk<P, MUON_F32>(T, v0, acc);
-    else if (T.dtype == MUON_BF16) partial_chunk<P, MUON_BF16>(T, v0, acc);
-    else partial_chunk<P, MUON_F16>(T, v0, acc);
+    ti = tensor_of(L.chunk0, L.n, c, ti);
+    norm_chunk_of<P>(L.t[ti], (long long)(c - L.chunk0[ti]) * GRAD_CHUNK_VECS, threadIdx.x, acc);
   }
-  acc = block_join<P>(acc, red);
-  if (threadIdx.x == 0) L.partials[L.part0 + blockIdx.x] = acc.word();
+  acc = block_join<P, GRAD_THREADS>(acc, red);
+  if (threadIdx.x == 0) L.h.partials[L.part0 + blockIdx.x] = acc.word();
 }
 
-// N and s from the partials, the same in every thread of every CTA that asks.
-// s is formed in fp64 from the unrounded N; a NaN norm gives a NaN scale.
-template <int P>
-__device__ __forceinline__ float finish(const GradLaunch& L, unsigned long long* red, float* norm) {
-  Acc<P> acc;
-  for (int i = threadIdx.x; i < L.npartials; i += GRAD_THREADS) {
-    Acc<P> x;
-    x.set(__ldcg(L.partials + i));
-    acc.join(x);
-  }
-  const double nrm = block_join<P>(acc, red).norm();
-  *norm = (float)nrm;
-  const double den = nrm + L.eps;
-  const double s = (isinf(L.max_norm) || den == 0.0) ? 1.0 : L.max_norm / den;
+// s from N, in fp64 and from the unrounded N; a NaN norm gives a NaN scale.
+__device__ __forceinline__ float scale_of(double norm, const GradCall& h) {
+  const double den = norm + h.eps;
+  const double s = (isinf(h.max_norm) || den == 0.0) ? 1.0 : h.max_norm / den;
   return s >= 1.0 ? 1.f : (float)s;
 }
 
+// N from the partials, the same in every thread of every CTA that asks.
 template <int P>
-__global__ void __launch_bounds__(GRAD_THREADS) grad_finish_kernel(const __grid_constant__ GradLaunch L) {
+__device__ __forceinline__ double joined(const GradCall& h, unsigned long long* red) {
+  Acc<P> acc;
+  for (int i = threadIdx.x; i < h.npartials; i += GRAD_THREADS) {
+    Acc<P> x;
+    x.set(__ldcg(h.partials + i));
+    acc.join(x);
+  }
+  return block_join<P, GRAD_THREADS>(acc, red).norm();
+}
+
+__device__ __forceinline__ double joined(const GradCall& h, unsigned long long* red) {
+  if (h.norm_kind == GRAD_L1) return joined<GRAD_L1>(h, red);
+  if (h.norm_kind == GRAD_L2) return joined<GRAD_L2>(h, red);
+  return joined<GRAD_INF>(h, red);
+}
+
+__device__ __forceinline__ void write_results(const GradCall& h, double norm, float s) {
+  *h.norm = (float)norm;
+  if (h.scale) *h.scale = s;
+}
+
+__global__ void __launch_bounds__(GRAD_THREADS) grad_finish_kernel(const __grid_constant__ GradCall h) {
   __shared__ unsigned long long red[GRAD_THREADS / 32];
-  float norm;
-  const float s = finish<P>(L, red, &norm);
-  if (threadIdx.x == 0) {
-    *L.norm = norm;
-    if (L.scale) *L.scale = s;
+  pdl_wait();
+  const double norm = joined(h, red);
+  if (threadIdx.x == 0) write_results(h, norm, scale_of(norm, h));
+}
+
+// ---------------------------------------------------------------- scaling
+__device__ __forceinline__ void st32(void* p, const uint32_t* r) {
+  asm volatile("st.global.cs.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+               :: "l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
+// Writes the E scaled elements of one vector.
+template <int OT, int E>
+__device__ __forceinline__ void store_vec(typename Elem<OT>::T* out, const float* f, float s, bool wide) {
+  typedef Elem<OT> Y;
+  constexpr int W = E * (int)sizeof(typename Y::T) / 4;   // words: 2, 4 or 8
+  uint32_t w[W];
+  if constexpr (OT == MUON_F32) {
+#pragma unroll
+    for (int k = 0; k < E; ++k) w[k] = __float_as_uint(__fmul_rn(s, f[k]));
+  } else {
+#pragma unroll
+    for (int k = 0; k < W; ++k) w[k] = Y::pack(__fmul_rn(s, f[2 * k]), __fmul_rn(s, f[2 * k + 1]));
+  }
+  if constexpr (W == 2) {
+    __stcs(reinterpret_cast<uint2*>(out), make_uint2(w[0], w[1]));
+  } else if constexpr (W == 4) {
+    __stcs(reinterpret_cast<uint4*>(out), make_uint4(w[0], w[1], w[2], w[3]));
+  } else {
+    if (wide) {
+      st32(out, w);
+    } else {
+      __stcs(reinterpret_cast<uint4*>(out), make_uint4(w[0], w[1], w[2], w[3]));
+      __stcs(reinterpret_cast<uint4*>(out) + 1, make_uint4(w[4], w[5], w[6], w[7]));
+    }
   }
 }
 
 template <int DT, int OT>
-__device__ __forceinline__ void scale_chunk(const GradTensor& T, long long v0, float s) {
+__device__ __forceinline__ void scale_chunk(const GradTensor& T, long long v0, int tid, float s) {
   typedef Elem<DT> X;
   typedef Elem<OT> Y;
   constexpr int E = X::E;
-  const typename X::T* g = reinterpret_cast<const typename X::T*>(T.g);
-  typename Y::T* out = reinterpret_cast<typename Y::T*>(T.out);
-  const long long nvec = (T.numel + T.mis + E - 1) / E;
-  uint4 raw[GRAD_VEC];
-  bool full[GRAD_VEC];
+  const typename X::T* g = reinterpret_cast<const typename X::T*>(T.g) - T.mis;   // of vector 0
+  typename Y::T* out = reinterpret_cast<typename Y::T*>(T.out) - T.mis;
+  const long long end = T.numel + T.mis;
+  if (T.out_vec && (v0 > 0 || T.mis == 0) && (v0 + GRAD_CHUNK_VECS) * E <= end) {
+    const uint4* p = reinterpret_cast<const uint4*>(g) + v0 + tid;
+    uint4 raw[GRAD_VEC];
 #pragma unroll
-  for (int j = 0; j < GRAD_VEC; ++j) {
-    const long long v = v0 + threadIdx.x + j * GRAD_THREADS;
-    const long long e = v * E - T.mis;
-    full[j] = e >= 0 && e + E <= T.numel;
-    raw[j] = make_uint4(0, 0, 0, 0);
-    if (full[j]) raw[j] = *reinterpret_cast<const uint4*>(g + e);
-  }
+    for (int j = 0; j < GRAD_VEC; ++j) raw[j] = __ldcs(p + j * GRAD_THREADS);
 #pragma unroll
-  for (int j = 0; j < GRAD_VEC; ++j) {
-    const long long v = v0 + threadIdx.x + j * GRAD_THREADS;
-    const long long e = v * E - T.mis;
-    if (full[j]) {
+    for (int j = 0; j < GRAD_VEC; ++j) {
       float f[E];
       X::unpack(raw[j], f);
-      union {
-        typename Y::T y[E];
-        uint4 q[sizeof(typename Y::T) * E / 16 > 0 ? sizeof(typename Y::T) * E / 16 : 1];
-        uint2 d;
-      } o;
-#pragma unroll
-      for (int k = 0; k < E; ++k) o.y[k] = Y::narrow(__fmul_rn(s, f[k]));
-      if (T.out_vec) {
-        if constexpr (sizeof(typename Y::T) * E >= 16) {
-#pragma unroll
-          for (int q = 0; q < (int)sizeof(typename Y::T) * E / 16; ++q)
-            reinterpret_cast<uint4*>(out + e)[q] = o.q[q];
-        } else {
-          *reinterpret_cast<uint2*>(out + e) = o.d;
-        }
-      } else {
-#pragma unroll
-        for (int k = 0; k < E; ++k) out[e + k] = o.y[k];
-      }
-    } else if (v < nvec) {
-      for (int k = 0; k < E; ++k)
-        if (e + k >= 0 && e + k < T.numel)
-          out[e + k] = Y::narrow(__fmul_rn(s, X::widen(g[e + k])));
+      store_vec<OT, E>(out + (v0 + tid + j * GRAD_THREADS) * E, f, s, T.out_vec > 1);
     }
+    return;
   }
+  if (T.out_vec) {
+    const long long v1 = min(v0 + GRAD_CHUNK_VECS, (end + E - 1) / E);
+    for (long long v = v0 + tid; v < v1; v += GRAD_THREADS) {
+      const long long e = v * E;
+      if (e >= T.mis && e + E <= end) {
+        float f[E];
+        X::unpack(__ldcs(reinterpret_cast<const uint4*>(g) + v), f);
+        store_vec<OT, E>(out + e, f, s, T.out_vec > 1);
+      } else {
+        for (int k = 0; k < E; ++k)
+          if (e + k >= T.mis && e + k < end) out[e + k] = Y::narrow(__fmul_rn(s, X::widen(g[e + k])));
+      }
+    }
+    return;
+  }
+  // The output is not aligned where the input is: single elements, neighbours
+  // in neighbouring threads.
+  const long long e1 = min((v0 + GRAD_CHUNK_VECS) * E, end);
+  for (long long e = max(v0 * E, (long long)T.mis) + tid; e < e1; e += GRAD_THREADS)
+    out[e] = Y::narrow(__fmul_rn(s, X::widen(g[e])));
 }
 
 template <int DT>
-__device__ __forceinline__ void scale_chunk_to(const GradTensor& T, long long v0, float s) {
-  if (T.out_dtype == MUON_F32) scale_chunk<DT, MUON_F32>(T, v0, s);
-  else if (T.out_dtype == MUON_BF16) scale_chunk<DT, MUON_BF16>(T, v0, s);
-  else scale_chunk<DT, MUON_F16>(T, v0, s);
+__device__ __forceinline__ void scale_chunk_to(const GradTensor& T, long long v0, int tid, float s) {
+  if (T.out_dtype == MUON_F32) scale_chunk<DT, MUON_F32>(T, v0, tid, s);
+  else if (T.out_dtype == MUON_BF16) scale_chunk<DT, MUON_BF16>(T, v0, tid, s);
+  else scale_chunk<DT, MUON_F16>(T, v0, tid, s);
 }
 
-template <int P>
-__global__ void __launch_bounds__(GRAD_THREADS) grad_scale_kernel(const __grid_constant__ GradLaunch L) {
+__device__ __forceinline__ void scale_chunk_of(const GradTensor& T, long long v0, int tid, float s) {
+  if (s == 1.f && T.out == T.g) return;   // in place and under the bound: 1 * g is g
+  if (T.dtype == MUON_F32) scale_chunk_to<MUON_F32>(T, v0, tid, s);
+  else if (T.dtype == MUON_BF16) scale_chunk_to<MUON_BF16>(T, v0, tid, s);
+  else scale_chunk_to<MUON_F16>(T, v0, tid, s);
+}
+
+// Chunks are taken from the last to the first: the norm read them in
+// ascending order, so the last ones are the ones still in L2.
+template <int N>
+__global__ void __launch_bounds__(GRAD_THREADS) grad_scale_kernel(const __grid_constant__ GradLaunch<N> L) {
   __shared__ unsigned long long red[GRAD_THREADS / 32];
-  float norm;
-  const float s = finish<P>(L, red, &norm);
-  if (blockIdx.x == 0 && threadIdx.x == 0) {
-    if (L.norm) *L.norm = norm;
-    if (L.scale) *L.scale = s;
-  }
-  int ti = 0;
-  for (int c = blockIdx.x; c < L.nchunks; c += gridDim.x) {
-    while (ti + 1 < L.n && L.t[ti + 1].chunk0 <= c) ++ti;
-    const GradTensor& T = L.t[ti];
-    if (s == 1.f && T.out == T.g) continue;   // in place and under the bound: 1 * g is g
-    const long long v0 = (long long)(c - T.chunk0) * GRAD_CHUNK_VECS;
-    if (T.dtype == MUON_F32) scale_chunk_to<MUON_F32>(T, v0, s);
-    else if (T.dtype == MUON_BF16) scale_chunk_to<MUON_BF16>(T, v0, s);
-    else scale_chunk_to<MUON_F16>(T, v0, s);
+  pdl_wait();
+  const double norm = joined(L.h, red);
+  const float s = scale_of(norm, L.h);
+  if (blockIdx.x == 0 && threadIdx.x == 0 && L.h.norm) write_results(L.h, norm, s);
+  if (s == 1.f && L.in_place) return;
+  for (int k = blockIdx.x; k < L.nchunks; k += gridDim.x) {
+    const int c = L.nchunks - 1 - k;
+    const int ti = tensor_of(L.chunk0, L.n, c, 0);
+    scale_chunk_of(L.t[ti], (long long)(c - L.chunk0[ti]) * GRAD_CHUNK_VECS, threadIdx.x, s);
   }
 }
 
+// ---------------------------------------------------------------- short lists: one cluster
+// Each CTA is CLUSTER_GROUPS groups of GRAD_THREADS threads; a group takes
+// every (groups of the cluster)-th chunk.
+constexpr int CLUSTER_GROUPS = GRAD_CLUSTER_THREADS / GRAD_THREADS;
+
 template <int P>
-cudaError_t launch(const GradLaunch& L, GradStage stage, int grid, cudaStream_t stream) {
-  if (stage == GRAD_STAGE_PARTIAL) grad_partial_kernel<P><<<grid, GRAD_THREADS, 0, stream>>>(L);
-  else if (stage == GRAD_STAGE_FINISH) grad_finish_kernel<P><<<1, GRAD_THREADS, 0, stream>>>(L);
-  else grad_scale_kernel<P><<<grid, GRAD_THREADS, 0, stream>>>(L);
-  return cudaGetLastError();
+__global__ void __launch_bounds__(GRAD_CLUSTER_THREADS, 1)
+    grad_cluster_kernel(const __grid_constant__ GradLaunch<GRAD_SHORT_TENSORS> L) {
+  __shared__ unsigned long long red[GRAD_CLUSTER_THREADS / 32];
+  __shared__ unsigned long long all[GRAD_CLUSTER_MAX];
+  cg::cluster_group cluster = cg::this_cluster();
+  const int rank = (int)cluster.block_rank(), ctas = (int)cluster.num_blocks();
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");   // this CTA has started
+  const int tid = threadIdx.x % GRAD_THREADS;
+  const int group = rank * CLUSTER_GROUPS + threadIdx.x / GRAD_THREADS, groups = ctas * CLUSTER_GROUPS;
+  Acc<P> acc;
+  int ti = 0;
+  for (int c = group; c < L.nchunks; c += groups) {
+    ti = tensor_of(L.chunk0, L.n, c, ti);
+    norm_chunk_of<P>(L.t[ti], (long long)(c - L.chunk0[ti]) * GRAD_CHUNK_VECS, tid, acc);
+  }
+  acc = block_join<P, GRAD_CLUSTER_THREADS>(acc, red);
+  asm volatile("barrier.cluster.wait.aligned;" ::: "memory");             // every CTA has
+  if (threadIdx.x < ctas) *cluster.map_shared_rank(&all[rank], threadIdx.x) = acc.word();
+  cluster.sync();   // every CTA's value is in every CTA's `all`
+  Acc<P> sum;
+  for (int r = 0; r < ctas; ++r) {
+    Acc<P> x;
+    x.set(all[r]);
+    sum.join(x);
+  }
+  const double norm = sum.norm();
+  const float s = scale_of(norm, L.h);
+  if (rank == 0 && threadIdx.x == 0) write_results(L.h, norm, s);
+  if (!L.scales) return;
+  ti = 0;
+  for (int c = group; c < L.nchunks; c += groups) {
+    ti = tensor_of(L.chunk0, L.n, c, ti);
+    scale_chunk_of(L.t[ti], (long long)(c - L.chunk0[ti]) * GRAD_CHUNK_VECS, tid, s);
+  }
+}
+
+template <class F, class... A>
+cudaError_t launch_with(F kernel, int grid, int threads, cudaStream_t stream, bool dependent, int cluster,
+                        const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  if (dependent) {
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+  } else {
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim = {(unsigned)cluster, 1, 1};
+  }
+  cfg.attrs = attr;
+  cfg.numAttrs = dependent || cluster > 0 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <int N>
+cudaError_t launch_partial(const GradLaunch<N>& L, int grid, cudaStream_t s) {
+  if (L.h.norm_kind == GRAD_L1) return launch_with(grad_partial_kernel<GRAD_L1, N>, grid, GRAD_THREADS, s, false, 0, L);
+  if (L.h.norm_kind == GRAD_L2) return launch_with(grad_partial_kernel<GRAD_L2, N>, grid, GRAD_THREADS, s, false, 0, L);
+  return launch_with(grad_partial_kernel<GRAD_INF, N>, grid, GRAD_THREADS, s, false, 0, L);
 }
 
 }  // namespace
 
-int grad_blocks_per_sm() {
-  int a = 0, b = 0;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&a, grad_partial_kernel<GRAD_L2>, GRAD_THREADS, 0) !=
-          cudaSuccess ||
-      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&b, grad_scale_kernel<GRAD_L2>, GRAD_THREADS, 0) !=
-          cudaSuccess)
-    return 1;
-  const int n = a < b ? a : b;
-  return n < 1 ? 1 : n;
+int grad_blocks_per_sm(bool scale) {
+  int n = 0;
+  const cudaError_t e =
+      scale ? cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, grad_scale_kernel<GRAD_MAX_TENSORS>, GRAD_THREADS, 0)
+            : cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, grad_partial_kernel<GRAD_L2, GRAD_MAX_TENSORS>,
+                                                            GRAD_THREADS, 0);
+  return e != cudaSuccess || n < 1 ? 1 : n;
 }
 
-cudaError_t launch_grad(const GradLaunch& L, int norm, GradStage stage, int grid, cudaStream_t stream) {
-  if (norm == GRAD_L1) return launch<GRAD_L1>(L, stage, grid, stream);
-  if (norm == GRAD_L2) return launch<GRAD_L2>(L, stage, grid, stream);
-  return launch<GRAD_INF>(L, stage, grid, stream);
+cudaError_t launch_grad_partial(const GradLaunch<GRAD_SHORT_TENSORS>& L, int grid, cudaStream_t stream) {
+  return launch_partial(L, grid, stream);
+}
+cudaError_t launch_grad_partial(const GradLaunch<GRAD_MAX_TENSORS>& L, int grid, cudaStream_t stream) {
+  return launch_partial(L, grid, stream);
+}
+cudaError_t launch_grad_scale(const GradLaunch<GRAD_SHORT_TENSORS>& L, int grid, cudaStream_t stream) {
+  return launch_with(grad_scale_kernel<GRAD_SHORT_TENSORS>, grid, GRAD_THREADS, stream, true, 0, L);
+}
+cudaError_t launch_grad_scale(const GradLaunch<GRAD_MAX_TENSORS>& L, int grid, cudaStream_t stream) {
+  return launch_with(grad_scale_kernel<GRAD_MAX_TENSORS>, grid, GRAD_THREADS, stream, true, 0, L);
+}
+cudaError_t launch_grad_finish(const GradCall& h, cudaStream_t stream) {
+  return launch_with(grad_finish_kernel, 1, GRAD_THREADS, stream, true, 0, h);
+}
+cudaError_t launch_grad_cluster(const GradLaunch<GRAD_SHORT_TENSORS>& L, int ctas, cudaStream_t stream) {
+  if (L.h.norm_kind == GRAD_L1)
+    return launch_with(grad_cluster_kernel<GRAD_L1>, ctas, GRAD_CLUSTER_THREADS, stream, false, ctas, L);
+  if (L.h.norm_kind == GRAD_L2)
+    return launch_with(grad_cluster_kernel<GRAD_L2>, ctas, GRAD_CLUSTER_THREADS, stream, false, ctas, L);
+  return launch_with(grad_cluster_kernel<GRAD_INF>, ctas, GRAD_CLUSTER_THREADS, stream, false, ctas, L);
 }
 
 }  // namespace muon

@@ -242,36 +242,49 @@ constexpr int GRAD_THREADS = 256;
 constexpr int GRAD_VEC = 4;                                    // vectors per thread and chunk
 constexpr int GRAD_CHUNK_VECS = GRAD_THREADS * GRAD_VEC;       // 16 KB
 constexpr int GRAD_MAX_TENSORS = 512;                          // per launch
-constexpr int GRAD_MAX_CTAS = 148 * 8;                         // partial sums of one launch
+constexpr int GRAD_SHORT_TENSORS = 64;                         // per launch with the short table
+constexpr int GRAD_MAX_CTAS = 148 * 8;                         // partial values of one launch
+// Lists of at most GRAD_CLUSTER_CHUNKS chunks take the one-cluster kernel.
+constexpr int GRAD_CLUSTER_CHUNKS = GRAD_SHORT_TENSORS;        // 1 MB
+constexpr int GRAD_CLUSTER_THREADS = 1024;
+constexpr int GRAD_CLUSTER_MAX = 8;                            // CTAs
 
 enum GradNorm : int { GRAD_L1 = 1, GRAD_L2 = 2, GRAD_INF = 3 };
-enum GradStage : int {
-  GRAD_STAGE_PARTIAL = 0,    // one partial sum per CTA
-  GRAD_STAGE_FINISH = 1,     // the norm and the scale from every partial sum
-  GRAD_STAGE_SCALE = 2,      // the same, and the gradients scaled
-};
 
 struct GradTensor {
   const void* g;
   void* out;                 // scaled gradients (may be g); unused for the norm alone
   long long numel;           // > 0
-  int chunk0;                // first chunk of this tensor in the launch
   unsigned char dtype;       // muon_dtype_t of g
   unsigned char out_dtype;   // muon_dtype_t of out
   unsigned char mis;         // elements of g past a 16-byte boundary
-  unsigned char out_vec;     // out is aligned for vector stores at g's vector starts
+  // how a vector's worth of out may be written: 0 by elements, 1 in 16-byte
+  // (or, where that is all of it, 8-byte) stores, 2 in one 32-byte store too
+  unsigned char out_vec;
 };
 
-struct GradLaunch {
-  int n;                     // tensors in this launch
-  int nchunks;               // chunks of all of them
-  int part0;                 // first partial sum this launch writes
-  int npartials;             // partial sums of all launches of the call
-  unsigned long long* partials;
-  float* norm;
+// What every launch of a call shares.
+struct GradCall {
+  unsigned long long* partials;   // one word per CTA of the partial launches
+  int npartials;                  // of all of them
+  int norm_kind;                  // GradNorm
+  float* norm;                    // results; nullptr: another launch writes them
   float* scale;
   double max_norm, eps;
-  GradTensor t[GRAD_MAX_TENSORS];
+};
+
+// One launch's tensors.  The table travels as a kernel argument, so a short
+// list goes with a short one.
+template <int N>
+struct GradLaunch {
+  GradCall h;
+  int n;                     // tensors in this launch
+  int nchunks;               // chunks of all of them
+  int part0;                 // first partial value this launch writes
+  int in_place;              // every out is its g
+  int scales;                // one-cluster kernel: scale as well
+  int chunk0[N];             // first chunk of each tensor in the launch
+  GradTensor t[N];
 };
 
 // ---------------------------------------------------------------- launchers
@@ -285,9 +298,13 @@ int k1_blocks_per_sm();
 cudaError_t launch_apply(const ApplyLaunch& L, cudaStream_t stream);
 cudaError_t launch_adamw(const AdamWLaunch& L, int grid, cudaStream_t stream);
 int adamw_blocks_per_sm();
-int grad_blocks_per_sm();
-// norm: a GradNorm.
-cudaError_t launch_grad(const GradLaunch& L, int norm, GradStage stage, int grid, cudaStream_t stream);
+int grad_blocks_per_sm(bool scale);
+cudaError_t launch_grad_partial(const GradLaunch<GRAD_SHORT_TENSORS>& L, int grid, cudaStream_t stream);
+cudaError_t launch_grad_partial(const GradLaunch<GRAD_MAX_TENSORS>& L, int grid, cudaStream_t stream);
+cudaError_t launch_grad_scale(const GradLaunch<GRAD_SHORT_TENSORS>& L, int grid, cudaStream_t stream);
+cudaError_t launch_grad_scale(const GradLaunch<GRAD_MAX_TENSORS>& L, int grid, cudaStream_t stream);
+cudaError_t launch_grad_finish(const GradCall& h, cudaStream_t stream);
+cudaError_t launch_grad_cluster(const GradLaunch<GRAD_SHORT_TENSORS>& L, int ctas, cudaStream_t stream);
 // The bound of every device-side wait, in ns (muon_set_wait_limit_ns, else
 // MUON_SPIN_LIMIT_NS at first use, else 2 s).  Takes the interface's lock.
 unsigned long long current_wait_limit_ns();

@@ -201,6 +201,7 @@ struct DeviceCtx {
   int k1_blocks_per_sm = 1;
   int adamw_blocks_per_sm = 1;
   int grad_blocks_per_sm = 1;
+  int grad_scale_blocks_per_sm = 1;
   int max_pairs = 1;           // co-resident CTA pairs of the GEMM kernels
   int* status = nullptr;
   std::map<std::vector<long long>, std::unique_ptr<Plan>> plans;
@@ -293,7 +294,8 @@ int get_ctx(DeviceCtx** out) {
   if (ctx->max_pairs < 1) ctx->max_pairs = std::max(1, prop.multiProcessorCount / 2);
   ctx->k1_blocks_per_sm = k1_blocks_per_sm();   // persistent: as many CTAs as fit
   ctx->adamw_blocks_per_sm = adamw_blocks_per_sm();
-  ctx->grad_blocks_per_sm = grad_blocks_per_sm();
+  ctx->grad_blocks_per_sm = grad_blocks_per_sm(false);
+  ctx->grad_scale_blocks_per_sm = grad_blocks_per_sm(true);
   *out = ctx.get();
   g_ctx[dev] = std::move(ctx);
   return MUON_OK;
@@ -1018,11 +1020,12 @@ int grad_norm_of(double p) {
   return 0;
 }
 
-// The number of launches that n tensors take: a launch ends when its table or
-// its chunk count is full.  The alignment is not known here, so every tensor
-// counts the vector that a bad alignment can add.
+// The number of launches that n tensors take, 0 for a list that one cluster
+// takes without a workspace: a launch ends when its table or its chunk count
+// is full.  The alignment is not known here, so every tensor counts the vector
+// that a bad alignment can add.
 long long grad_launches(const unsigned char* dtypes, const int64_t* numels, int n) {
-  long long launches = 0, chunks = 0;
+  long long launches = 0, chunks = 0, all = 0;
   int held = 0;
   for (int i = 0; i < n; ++i) {
     if (numels[i] == 0) continue;
@@ -1034,8 +1037,9 @@ long long grad_launches(const unsigned char* dtypes, const int64_t* numels, int 
     }
     ++held;
     chunks += c;
+    all += c;
   }
-  return launches;
+  return all <= GRAD_CLUSTER_CHUNKS ? 0 : launches;
 }
 
 int check_grad_list(const void* const* ptrs, const unsigned char* dtypes, const int64_t* numels, int n) {
@@ -1049,73 +1053,123 @@ int check_grad_list(const void* const* ptrs, const unsigned char* dtypes, const 
   return MUON_OK;
 }
 
-// The launches of a norm (outs == nullptr) or of a clip.
-int run_grad(const void* const* grads, const unsigned char* dtypes, const int64_t* numels, int n,
-             void* const* outs, const unsigned char* out_dtypes, int norm_kind, double max_norm,
-             double eps, float* norm, float* scale, void* workspace, cudaStream_t stream) {
+// A norm (outs == nullptr) or a clip of one list.
+struct GradList {
+  const void* const* grads;
+  const unsigned char* dtypes;
+  const int64_t* numels;
+  int n;
+  void* const* outs;
+  const unsigned char* out_dtypes;
+};
+
+int grad_mis(const GradList& a, int i) {
+  return (int)((reinterpret_cast<uintptr_t>(a.grads[i]) & 15u) / dtype_size(a.dtypes[i]));
+}
+
+GradTensor grad_tensor(const GradList& a, int i) {
+  GradTensor T;
+  T.g = a.grads[i];
+  T.out = a.outs ? a.outs[i] : nullptr;
+  T.numel = a.numels[i];
+  T.dtype = a.dtypes[i];
+  T.out_dtype = a.outs ? a.out_dtypes[i] : a.dtypes[i];
+  T.mis = (unsigned char)grad_mis(a, i);
+  const int size = dtype_size(T.out_dtype), bytes = 16 / dtype_size(T.dtype) * size;   // of a vector's worth
+  const uintptr_t at = reinterpret_cast<uintptr_t>(T.out) - (uintptr_t)(T.mis * size);
+  T.out_vec = at % std::min(16, bytes) ? 0 : bytes == 32 && at % 32 == 0 ? 2 : 1;
+  return T;
+}
+
+// Fills launches of at most N tensors and kGradMaxChunks chunks from the list
+// and passes each, when it is full or the last, to `go`.
+template <int N, class F>
+int grad_walk(const GradList& a, GradLaunch<N>& L, F go) {
+  L.n = 0;
+  L.nchunks = 0;
+  L.in_place = 1;
+  for (int i = 0; i < a.n; ++i) {
+    if (a.numels[i] == 0) continue;
+    const long long chunks = grad_chunks(a.numels[i], grad_mis(a, i), a.dtypes[i]);
+    if (L.n == N || L.nchunks + chunks > kGradMaxChunks) {
+      const int rc = go();
+      if (rc) return rc;
+      L.n = 0;
+      L.nchunks = 0;
+      L.in_place = 1;
+    }
+    L.chunk0[L.n] = L.nchunks;
+    L.t[L.n] = grad_tensor(a, i);
+    L.in_place &= L.t[L.n].out == L.t[L.n].g;
+    ++L.n;
+    L.nchunks += (int)chunks;
+  }
+  return L.n > 0 ? go() : MUON_OK;
+}
+
+template <int N>
+int run_grad_long(DeviceCtx* ctx, const GradList& a, const GradCall& call, cudaStream_t stream) {
+  static thread_local GradLaunch<N> L;
+  L.h = call;
+  L.h.npartials = 0;
+  L.scales = 0;
+  const int most = std::min(GRAD_MAX_CTAS, ctx->num_sms * ctx->grad_blocks_per_sm);
+  int rc = grad_walk(a, L, [&]() -> int {
+    const int grid = std::min(L.nchunks, most);
+    L.part0 = L.h.npartials;
+    L.h.npartials += grid;
+    ProfScope ps(PK_GRAD_NORM, stream);
+    return cuda_err(launch_grad_partial(L, grid, stream));
+  });
+  if (rc) return rc;
+  if (!a.outs || L.h.npartials == 0) {
+    ProfScope ps(PK_GRAD_NORM, stream);
+    return cuda_err(launch_grad_finish(L.h, stream));
+  }
+  // One table holds the whole list: it still stands; else it is filled again.
+  auto scale = [&]() -> int {
+    const int grid = std::min(L.nchunks, ctx->num_sms * ctx->grad_scale_blocks_per_sm);
+    ProfScope ps(PK_GRAD_SCALE, stream);
+    const int r = cuda_err(launch_grad_scale(L, grid, stream));
+    L.h.norm = nullptr;   // written by the first scaling launch
+    return r;
+  };
+  return L.part0 == 0 ? scale() : grad_walk(a, L, scale);
+}
+
+int run_grad(const GradList& a, const GradCall& call, cudaStream_t stream) {
   std::lock_guard<std::mutex> lock(g_mutex);
   DeviceCtx* ctx = nullptr;
   int rc = get_ctx(&ctx);
   if (rc) return rc;
-  const int max_grid = std::min(GRAD_MAX_CTAS, ctx->num_sms * ctx->grad_blocks_per_sm);
-  static thread_local GradLaunch L;
-  L.partials = static_cast<unsigned long long*>(workspace);
-  L.max_norm = max_norm;
-  L.eps = eps;
-  L.npartials = 0;
-  // Walks the tensors launch by launch.  The scaling launches come after all
-  // of the norm's, so the tables are built a second time for them.
-  auto walk = [&](GradStage stage, float* out_norm, float* out_scale) -> int {
-    L.norm = out_norm;
-    L.scale = out_scale;
+  long long chunks = 0;
+  int held = 0;
+  for (int i = 0; i < a.n && chunks <= GRAD_CLUSTER_CHUNKS; ++i) {
+    if (a.numels[i] == 0) continue;
+    ++held;
+    chunks += grad_chunks(a.numels[i], grad_mis(a, i), a.dtypes[i]);
+  }
+  if (chunks <= GRAD_CLUSTER_CHUNKS) {
+    static thread_local GradLaunch<GRAD_SHORT_TENSORS> L;
+    L.h = call;
+    L.part0 = 0;
+    L.scales = a.outs != nullptr;
+    auto go = [&]() -> int {
+      int ctas = 1;
+      while (ctas < GRAD_CLUSTER_MAX && ctas * (GRAD_CLUSTER_THREADS / GRAD_THREADS) < L.nchunks) ctas *= 2;
+      ProfScope ps(a.outs ? PK_GRAD_SCALE : PK_GRAD_NORM, stream);
+      return cuda_err(launch_grad_cluster(L, ctas, stream));
+    };
+    if (held > 0) return grad_walk(a, L, go);
     L.n = 0;
     L.nchunks = 0;
-    auto flush = [&]() -> int {
-      if (L.n == 0) return MUON_OK;
-      const int grid = std::max(1, std::min(L.nchunks, max_grid));
-      if (stage == GRAD_STAGE_PARTIAL) {
-        L.part0 = L.npartials;
-        L.npartials += grid;
-      }
-      ProfScope ps(stage == GRAD_STAGE_PARTIAL ? PK_GRAD_NORM : PK_GRAD_SCALE, stream);
-      const int r = cuda_err(launch_grad(L, norm_kind, stage, grid, stream));
-      L.norm = nullptr;    // written by the first scaling launch
-      L.scale = nullptr;
-      L.n = 0;
-      L.nchunks = 0;
-      return r;
-    };
-    for (int i = 0; i < n; ++i) {
-      if (numels[i] == 0) continue;
-      const int size = dtype_size(dtypes[i]), E = 16 / size;
-      const int mis = (int)((reinterpret_cast<uintptr_t>(grads[i]) & 15u) / size);
-      const long long chunks = grad_chunks(numels[i], mis, dtypes[i]);
-      if (L.n == GRAD_MAX_TENSORS || L.nchunks + chunks > kGradMaxChunks) {
-        const int r = flush();
-        if (r) return r;
-      }
-      GradTensor& T = L.t[L.n++];
-      T.g = grads[i];
-      T.out = outs ? outs[i] : nullptr;
-      T.numel = numels[i];
-      T.chunk0 = L.nchunks;
-      T.dtype = dtypes[i];
-      T.out_dtype = outs ? out_dtypes[i] : dtypes[i];
-      T.mis = (unsigned char)mis;
-      const int out_size = dtype_size(T.out_dtype);
-      T.out_vec = (reinterpret_cast<uintptr_t>(T.out) - (uintptr_t)(mis * out_size)) %
-                      std::min(16, E * out_size) == 0;
-      L.nchunks += (int)chunks;
-    }
-    return flush();
-  };
-  rc = walk(GRAD_STAGE_PARTIAL, nullptr, nullptr);
-  if (rc) return rc;
-  if (outs && L.npartials > 0) return walk(GRAD_STAGE_SCALE, norm, scale);
-  L.norm = norm;
-  L.scale = scale;
-  ProfScope ps(PK_GRAD_NORM, stream);
-  return cuda_err(launch_grad(L, norm_kind, GRAD_STAGE_FINISH, 1, stream));
+    L.in_place = 1;
+    return go();
+  }
+  for (int i = 0, k = 0; i < a.n; ++i)
+    if (a.numels[i] > 0 && ++k > GRAD_SHORT_TENSORS)
+      return run_grad_long<GRAD_MAX_TENSORS>(ctx, a, call, stream);
+  return run_grad_long<GRAD_SHORT_TENSORS>(ctx, a, call, stream);
 }
 
 }  // namespace
@@ -1287,7 +1341,7 @@ int64_t muon_grad_workspace_bytes(const unsigned char* dtypes, const int64_t* nu
   if (n < 0 || (n > 0 && (!dtypes || !numels))) return -1;
   for (int i = 0; i < n; ++i)
     if (numels[i] < 0 || numels[i] > kGradMaxNumel || dtypes[i] > MUON_F16) return -1;
-  return std::max(1ll, grad_launches(dtypes, numels, n)) * GRAD_MAX_CTAS * 8;
+  return grad_launches(dtypes, numels, n) * GRAD_MAX_CTAS * 8;
 }
 
 int muon_grad_norm(const void* const* grads, const unsigned char* dtypes, const int64_t* numels, int n,
@@ -1301,7 +1355,7 @@ int muon_clip_grads(const void* const* grads, const unsigned char* dtypes, const
                     void* const* outs, const unsigned char* out_dtypes, double p, double max_norm,
                     double eps, float* norm, float* scale, void* workspace, int64_t workspace_bytes,
                     void* stream) {
-  if (n < 0 || !norm || !workspace) return MUON_ERR_INVALID_ARG;
+  if (n < 0 || !norm) return MUON_ERR_INVALID_ARG;
   const int kind = grad_norm_of(p);
   if (kind == 0 || std::isnan(max_norm) || max_norm < 0 || !std::isfinite(eps) || eps < 0)
     return MUON_ERR_INVALID_ARG;
@@ -1314,11 +1368,18 @@ int muon_clip_grads(const void* const* grads, const unsigned char* dtypes, const
   if ((reinterpret_cast<uintptr_t>(norm) & 3u) || !scale_ok(scale) ||
       (reinterpret_cast<uintptr_t>(workspace) & 7u))
     return MUON_ERR_UNSUPPORTED;
-  if (workspace_bytes < muon_grad_workspace_bytes(dtypes, numels, n)) return MUON_ERR_INVALID_ARG;
-  return guarded([&] {
-    return run_grad(grads, dtypes, numels, n, outs, out_dtypes, kind, max_norm, eps, norm, scale,
-                    workspace, static_cast<cudaStream_t>(stream));
-  });
+  const int64_t need = muon_grad_workspace_bytes(dtypes, numels, n);
+  if (workspace_bytes < need || (need > 0 && !workspace)) return MUON_ERR_INVALID_ARG;
+  const GradList list = {grads, dtypes, numels, n, outs, out_dtypes};
+  GradCall call;
+  call.partials = static_cast<unsigned long long*>(workspace);
+  call.npartials = 0;
+  call.norm_kind = kind;
+  call.norm = norm;
+  call.scale = scale;
+  call.max_norm = max_norm;
+  call.eps = eps;
+  return guarded([&] { return run_grad(list, call, static_cast<cudaStream_t>(stream)); });
 }
 
 int muon_orthogonalize(const float* x, void* out, int out_is_bf16, int64_t rows, int64_t cols,

@@ -606,10 +606,28 @@ def test_scaled_norm_and_cast_match_the_stage_oracle(muon):
 
 
 def test_profiler_counts_the_launches(muon):
-    g = torch.ones(100000, device="cuda")
-    group = muon.GradGroup([g], out=[torch.empty_like(g)])
-    muon.profile_begin()
-    group.norm()
-    group.clip(1.0)
-    prof = muon.profile_end()
-    assert prof["grad_norm"][1] >= 2 and prof["grad_norm"][1] + prof["grad_scale"][1] >= 3
+    """One launch for a short list; the norm's two, or its first and the
+    scaling, for a long one."""
+    for n, norms, scales in ((100_000, 1, 1), (3_000_000, 3, 1)):
+        g = torch.ones(n, device="cuda")
+        group = muon.GradGroup([g], out=[torch.empty_like(g)])
+        muon.profile_begin()
+        group.norm()
+        group.clip(1.0)
+        prof = muon.profile_end()
+        assert prof["grad_norm"][1] == norms and prof["grad_scale"][1] == scales
+
+
+def test_around_the_border_of_the_two_forms(muon):
+    """64 chunks of 16 KB: the longest list of one cluster, and one vector more;
+    64 and 65 small tensors."""
+    n = 64 * 4096
+    for sizes in ([n], [n + 1], [n - 1], [n - 4096, 4096], [n - 4096, 4097], [5] * 64, [5] * 65, [0] * 9 + [n]):
+        gs, bases = _grads(sizes, [torch.float32], seed=80)
+        outs, obases = _grads(sizes, [torch.bfloat16], seed=81, offs=[8])
+        for p in (1.0, 2.0, INF):
+            _norm_ok(muon.grad_norm(gs, p), gs, p)
+        _check_clip(muon, gs, 1.0, outs=outs)
+        _check_clip(muon, gs, 1.0)
+        _guards_hold(bases)
+        _guards_hold(obases)

@@ -50,7 +50,7 @@ def test_refusals_of_the_c_entry_points(muon, call):
     assert call(lib, args=_args(ptr=None)) == -1
     assert call(lib, args=_args(ptr=66)) == -2                       # not a float address
     assert call(lib, args=_args(ptr=65, dtype=1)) == -2              # not a bf16 address
-    assert call(lib, bytes_=8) == -1                                 # workspace too small
+    assert call(lib, args=_args(numel=1 << 20), bytes_=8) == -1      # workspace too small
     g, t, ne = _args()
     assert lib.muon_grad_norm(None, t, ne, 1, 2.0, 1.0, 0.0, P(64), None, P(64), 1 << 20, None) == -1
     assert lib.muon_grad_norm(g, None, ne, 1, 2.0, 1.0, 0.0, P(64), None, P(64), 1 << 20, None) == -1
@@ -59,7 +59,7 @@ def test_refusals_of_the_c_entry_points(muon, call):
 
 def test_refusals_of_results_and_outputs(muon):
     lib = muon.library()
-    assert _norm(lib, norm=None) == -1 and _norm(lib, work=None) == -1
+    assert _norm(lib, norm=None) == -1 and _norm(lib, args=_args(numel=1 << 20), work=None) == -1
     assert _norm(lib, norm=66) == -2 and _norm(lib, scale=66) == -2 and _norm(lib, work=68) == -2
     assert _clip(lib, outs=(P * 1)(P(None))) == -1
     assert _clip(lib, outs=(P * 1)(P(130))) == -2
@@ -91,9 +91,10 @@ def test_workspace_bytes_counts_the_launches(muon):
         t = (ctypes.c_ubyte * max(n, 1))(*(dtypes or [0] * n))
         return lib.muon_grad_workspace_bytes(t, (ctypes.c_int64 * max(n, 1))(*numels), n)
 
-    one = ask([10])
+    one = ask([1 << 24])
     assert one > 0 and one % 8 == 0
-    assert ask([]) == one and ask([0, 0]) == one
+    assert ask([]) == 0 and ask([0, 0]) == 0 and ask([10]) == 0      # one cluster needs none
+    assert ask([7] * 64) == 0 and ask([7] * 65) == one
     assert ask([7] * 512) == one and ask([7] * 513) == 2 * one
     assert ask([0] * 100 + [7] * 512) == one                         # empty tensors take no place
     assert ask([1 << 40, 1 << 40, 1 << 40, 1 << 40, 1 << 40]) > one  # chunk count of one launch
