@@ -86,8 +86,8 @@ def library() -> ctypes.CDLL:
         "muon_step_mirrored": (i, [_PP, _PP, _PP, _I64P, i, f, f, i, i, _FP, _PP, i, _P]),
         "muon_guard_check": (i64, []),
         "muon_grad_workspace_bytes": (i64, [_P, _I64P, i]),
-        "muon_grad_norm": (i, [_PP, _P, _I64P, i, d, d, d, _P, _P, _P, i64, _P]),
-        "muon_clip_grads": (i, [_PP, _P, _I64P, i, _PP, _P, d, d, d, _P, _P, _P, i64, _P]),
+        "muon_grad_norm": (i, [_P, _P, _P, i, d, d, d, _P, _P, _P, i64, _P]),
+        "muon_clip_grads": (i, [_P, _P, _P, i, _P, _P, d, d, d, _P, _P, _P, i64, _P]),
         "muon_step_scaled": (i, [_PP, _PP, _PP, _I64P, i, f, f, i, i, _FP, _PP, i, _P, _P]),
         "muon_adamw_step_scaled": (i, [_PP, _PP, _PP, _PP, _I64P, _P, i, i64, d, d, d, d, d, _P, _P]),
         "muon_momentum_normalize_scaled": (i, [_PP, _PP, _PP, _I64P, _I64P, i, f, i, _P, _P]),
@@ -105,14 +105,19 @@ def _check(code: int, what: str):
         raise MuonError(code, what)
 
 
-# The current stream's handle without building a Stream object (0.1 instead of
-# 3.2 us per call), where this torch has it.
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+def _raw_stream(device: int) -> int:
+    """Handle of torch's current stream on a device."""
+    return int(torch.cuda.current_stream(device).cuda_stream)
+
+
+# The same without building a Stream object (0.1 instead of 3.2 us per call),
+# where this torch has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
 
 
 def _stream_ptr(stream) -> int:
     if stream is None:
-        if _raw_stream is not None and torch.cuda.is_initialized():
+        if torch.cuda.is_initialized():
             return _raw_stream(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
@@ -405,7 +410,13 @@ class GradGroup:
         self._clippable = self._disjoint(grads, grads if out is None else out)
         if self._device is None:
             self._device = torch.cuda.current_device()
-        self._like = torch.empty(1, dtype=torch.float32, device=torch.device("cuda", self._device))
+        # what the calls' results and workspaces are made like
+        device = torch.device("cuda", self._device)
+        self._result = torch.empty((), dtype=torch.float32, device=device)
+        self._work = torch.empty(self._bytes, dtype=torch.uint8, device=device) if self._bytes else None
+        at = ctypes.addressof
+        self._args = (at(self._g), at(self._gt), at(self._numels), n, None, None)
+        self._clip_args = self._args[:4] + (at(self._o), at(self._ot))
 
     @staticmethod
     def _disjoint(grads, outs) -> bool:
@@ -427,41 +438,42 @@ class GradGroup:
             ends[written] = max(ends[written], e)
         return True
 
-    def _call(self, clip, p, max_norm, eps, with_scale, stream):
-        _check_device(self._device, "grads")
-        if stream is not None and _stream_ptr(stream) != _stream_ptr(None):
+    def _call(self, args, p, max_norm, eps, with_scale, stream):
+        if torch.cuda.current_device() != self._device:
+            _check_device(self._device, "grads")
+        current = _raw_stream(self._device)
+        if stream is not None and _stream_ptr(stream) != current:
             if not isinstance(stream, torch.cuda.Stream):
                 ptr = _stream_ptr(stream)
                 stream = torch.cuda.ExternalStream(ptr) if ptr else torch.cuda.default_stream()
             with torch.cuda.stream(stream):     # the allocations below belong to that stream
-                return self._call(clip, p, max_norm, eps, with_scale, None)
-        norm = self._like.new_empty(())
-        scale = self._like.new_empty(()) if with_scale else None
-        work = self._like.new_empty(self._bytes // 4) if self._bytes else None
+                return self._call(args, p, max_norm, eps, with_scale, None)
+        norm = torch.empty_like(self._result)
+        scale = torch.empty_like(self._result) if with_scale else None
+        work = None if self._work is None else torch.empty_like(self._work)
         code = library().muon_clip_grads(
-            self._g, self._gt, self._numels, self._n, self._o if clip else None,
-            self._ot if clip else None, p, max_norm, eps, norm.data_ptr(),
-            None if scale is None else scale.data_ptr(), None if work is None else work.data_ptr(),
-            self._bytes, _stream_ptr(None))
-        _check(code, "muon_clip_grads" if clip else "muon_grad_norm")
+            *args, p, max_norm, eps, norm.data_ptr(), None if scale is None else scale.data_ptr(),
+            None if work is None else work.data_ptr(), self._bytes, current)
+        if code:
+            raise MuonError(code, "muon_grad_norm" if args is self._args else "muon_clip_grads")
         return (norm, scale) if with_scale else norm
 
     def norm(self, norm_type: float = 2.0, stream=None) -> torch.Tensor:
         """The norm over every gradient of the group, as a 0-d fp32 tensor.
         ``norm_type``: 1, 2 or inf (the largest magnitude)."""
-        return self._call(False, norm_type, _INF, 0.0, False, stream)
+        return self._call(self._args, norm_type, _INF, 0.0, False, stream)
 
     def clip_scale(self, max_norm: float, norm_type: float = 2.0, eps: float = 1e-6, stream=None):
         """(norm, scale): the norm, and min(1, max_norm / (norm + eps)) to be
         passed to the steps as ``grad_scale``.  Both 0-d fp32 tensors."""
-        return self._call(False, norm_type, max_norm, eps, True, stream)
+        return self._call(self._args, norm_type, max_norm, eps, True, stream)
 
     def clip(self, max_norm: float, norm_type: float = 2.0, eps: float = 1e-6, stream=None) -> torch.Tensor:
         """Multiplies every gradient by min(1, max_norm / (norm + eps)), in
         place or into ``out``, and returns the norm they had."""
         if not self._clippable:
             raise ValueError("tensors that clip writes must not overlap other tensors of the group")
-        return self._call(True, norm_type, max_norm, eps, False, stream)
+        return self._call(self._clip_args, norm_type, max_norm, eps, False, stream)
 
 
 def grad_norm(grads: Sequence[torch.Tensor], norm_type: float = 2.0, stream=None) -> torch.Tensor:
@@ -508,20 +520,22 @@ def momentum_normalize(grads, bufs, beta=0.95, nesterov=True, stream=None, grad_
     """The fused first kernel alone; returns oriented bf16 X0 views (m x n).
     ``grad_scale`` as for step."""
     n = len(grads)
-    x0s, lds, shapes, outs = [], [], [], []
+    lds, shapes, outs = [], [], []
     for g, b in zip(grads, bufs):
         _check_mat(g, "grad")
         _check_mat(b, "buf")
+        if b.shape != g.shape:
+            raise ValueError("grad and buf shapes differ")
         r, c = g.shape
-        m, nn = min(r, c), max(r, c)
+        m, nn = (r, c) if r <= c else (c, r)
         ld = _ld8(nn)
-        x = torch.empty((m, ld), dtype=torch.bfloat16, device=g.device)
-        x0s.append(x)
-        outs.append(x[:, :nn])
+        # rows of ld elements, as a view of their first nn
+        x = torch.empty_strided((m, nn), (ld, 1), dtype=torch.bfloat16, device=g.device)
+        outs.append(x)
         lds.append(ld)
-        shapes += [r, c]
+        shapes += (r, c)
     code = library().muon_momentum_normalize_scaled(
-        _ptr_array(grads), _ptr_array(bufs), _ptr_array(x0s), (ctypes.c_int64 * n)(*lds),
+        _ptr_array(grads), _ptr_array(bufs), _ptr_array(outs), (ctypes.c_int64 * n)(*lds),
         (ctypes.c_int64 * len(shapes))(*shapes), n, float(beta), int(bool(nesterov)),
         _scale_ptr(grad_scale), _stream_ptr(stream))
     _check(code, "muon_momentum_normalize")

@@ -149,9 +149,11 @@ __device__ __forceinline__ Acc<P> block_join(Acc<P> a, unsigned long long* red) 
 // [v E - mis, (v + 1) E - mis).  Only the first and the last can be partial;
 // those are read element by element, so nothing outside the tensor is touched.
 
-// The tensor that holds chunk c, from lo on: chunk0 ascends.
+// The tensor that holds chunk c, from lo on (chunk0 ascends): mostly the one
+// that held the last chunk.
 __device__ __forceinline__ int tensor_of(const int* chunk0, int n, int c, int lo) {
   int hi = n;
+  if (lo + 1 >= n || chunk0[lo + 1] > c) return lo;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (chunk0[mid] <= c) lo = mid;
@@ -160,34 +162,60 @@ __device__ __forceinline__ int tensor_of(const int* chunk0, int n, int c, int lo
   return lo;
 }
 
+// Whether chunk v0.. of the tensor is nothing but whole vectors.
+__device__ __forceinline__ bool whole_chunk(const GradTensor& T, long long v0) {
+  const int shift = T.dtype == MUON_F32 ? 2 : 3;   // log2 of a vector's elements
+  return (v0 > 0 || T.mis == 0) && ((v0 + GRAD_CHUNK_VECS) << shift) <= T.numel + T.mis;
+}
+
+// The 16-byte boundary at or before the first element.
+__device__ __forceinline__ const char* vector0(const GradTensor& T) {
+  return reinterpret_cast<const char*>(reinterpret_cast<uintptr_t>(T.g) & ~(uintptr_t)15);
+}
+
+struct Raw {
+  uint4 v[GRAD_VEC];
+};
+
+// (Coherent loads: in place, the scaling writes what it reads here.)
+template <bool STREAMED>
+__device__ __forceinline__ void load_chunk(const GradTensor& T, long long v0, int tid, Raw& r) {
+  const uint4* p = reinterpret_cast<const uint4*>(vector0(T)) + v0 + tid;
+#pragma unroll
+  for (int j = 0; j < GRAD_VEC; ++j) r.v[j] = STREAMED ? __ldcs(p + j * GRAD_THREADS) : p[j * GRAD_THREADS];
+}
+
 template <int P, int DT>
-__device__ __forceinline__ void norm_chunk(const GradTensor& T, long long v0, int tid, Acc<P>& acc) {
+__device__ __forceinline__ void add_vec(const uint4& v, Acc<P>& acc) {
+  float f[Elem<DT>::E];
+  Elem<DT>::unpack(v, f);
+#pragma unroll
+  for (int k = 0; k < Elem<DT>::E; ++k) acc.add(f[k]);
+}
+
+template <int P>
+__device__ __forceinline__ void add_raw(const Raw& r, int dtype, Acc<P>& acc) {
+#pragma unroll
+  for (int j = 0; j < GRAD_VEC; ++j) {
+    if (dtype == MUON_F32) add_vec<P, MUON_F32>(r.v[j], acc);
+    else if (dtype == MUON_BF16) add_vec<P, MUON_BF16>(r.v[j], acc);
+    else add_vec<P, MUON_F16>(r.v[j], acc);
+  }
+}
+
+// A chunk with a partial vector, or the last one of a tensor.
+template <int P, int DT>
+__device__ __forceinline__ void add_ragged(const GradTensor& T, long long v0, int tid, Acc<P>& acc) {
   typedef Elem<DT> X;
   constexpr int E = X::E;
-  const typename X::T* g = reinterpret_cast<const typename X::T*>(T.g) - T.mis;   // of vector 0
-  if ((v0 > 0 || T.mis == 0) && (v0 + GRAD_CHUNK_VECS) * E <= T.numel + T.mis) {
-    const uint4* p = reinterpret_cast<const uint4*>(g) + v0 + tid;
-    uint4 raw[GRAD_VEC];
-#pragma unroll
-    for (int j = 0; j < GRAD_VEC; ++j) raw[j] = __ldg(p + j * GRAD_THREADS);
-#pragma unroll
-    for (int j = 0; j < GRAD_VEC; ++j) {
-      float f[E];
-      X::unpack(raw[j], f);
-#pragma unroll
-      for (int k = 0; k < E; ++k) acc.add(f[k]);
-    }
-    return;
-  }
+  const typename X::T* g = reinterpret_cast<const typename X::T*>(vector0(T));
   const long long end = T.numel + T.mis;   // elements are counted from vector 0 here
   const long long v1 = min(v0 + GRAD_CHUNK_VECS, (end + E - 1) / E);
+#pragma unroll 4
   for (long long v = v0 + tid; v < v1; v += GRAD_THREADS) {
     const long long e = v * E;
     if (e >= T.mis && e + E <= end) {
-      float f[E];
-      X::unpack(__ldg(reinterpret_cast<const uint4*>(g) + v), f);
-#pragma unroll
-      for (int k = 0; k < E; ++k) acc.add(f[k]);
+      add_vec<P, DT>(__ldg(reinterpret_cast<const uint4*>(g) + v), acc);
     } else {
       for (int k = 0; k < E; ++k)
         if (e + k >= T.mis && e + k < end) acc.add(X::widen(g[e + k]));
@@ -195,28 +223,50 @@ __device__ __forceinline__ void norm_chunk(const GradTensor& T, long long v0, in
   }
 }
 
-template <int P>
-__device__ __forceinline__ void norm_chunk_of(const GradTensor& T, long long v0, int tid, Acc<P>& acc) {
-  if (T.dtype == MUON_F32) norm_chunk<P, MUON_F32>(T, v0, tid, acc);
-  else if (T.dtype == MUON_BF16) norm_chunk<P, MUON_BF16>(T, v0, tid, acc);
-  else norm_chunk<P, MUON_F16>(T, v0, tid, acc);
+// Chunks c, c + step, ... below `end`; STREAMED: not to be kept in L2.
+template <int P, bool STREAMED, int N>
+__device__ __forceinline__ int add_chunks_to(const GradLaunch<N>& L, int c, int step, int end, int tid, int& ti,
+                                             Acc<P>& acc) {
+  for (; c < end; c += step) {
+    ti = tensor_of(L.chunk0, L.n, c, ti);
+    const GradTensor& T = L.t[ti];
+    const long long v0 = (long long)(c - L.chunk0[ti]) * GRAD_CHUNK_VECS;
+    if (whole_chunk(T, v0)) {
+      Raw raw;
+      load_chunk<STREAMED>(T, v0, tid, raw);
+      add_raw<P>(raw, T.dtype, acc);
+    } else if (T.dtype == MUON_F32) {
+      add_ragged<P, MUON_F32>(T, v0, tid, acc);
+    } else if (T.dtype == MUON_BF16) {
+      add_ragged<P, MUON_BF16>(T, v0, tid, acc);
+    } else {
+      add_ragged<P, MUON_F16>(T, v0, tid, acc);
+    }
+  }
+  return c;
+}
+
+// The norm's part of chunks first, first + step, ... of the launch.  Where the
+// gradients are scaled afterwards, the chunks that the scaling reads first (the
+// last ones) are left in L2 by passing the ones before through as streamed.
+template <int P, int N>
+__device__ __forceinline__ Acc<P> add_chunks(const GradLaunch<N>& L, int first, int step, int tid) {
+  Acc<P> acc;
+  int ti = 0, c = first;
+  if (L.scales) c = add_chunks_to<P, true>(L, c, step, L.nchunks - GRAD_KEEP_CHUNKS, tid, ti, acc);
+  add_chunks_to<P, false>(L, c, step, L.nchunks, tid, ti, acc);
+  return acc;
 }
 
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 template <int P, int N>
-__global__ void __launch_bounds__(GRAD_THREADS, 4)
+__global__ void __launch_bounds__(GRAD_THREADS)
     grad_partial_kernel(const __grid_constant__ GradLaunch<N> L) {
   __shared__ unsigned long long red[GRAD_THREADS / 32];
   pdl_launch();
-  Acc<P> acc;
-  int ti = 0;
-  for (int c = blockIdx.x; c < L.nchunks; c += gridDim.x) {
-    ti = tensor_of(L.chunk0, L.n, c, ti);
-    norm_chunk_of<P>(L.t[ti], (long long)(c - L.chunk0[ti]) * GRAD_CHUNK_VECS, threadIdx.x, acc);
-  }
-  acc = block_join<P, GRAD_THREADS>(acc, red);
+  const Acc<P> acc = block_join<P, GRAD_THREADS>(add_chunks<P>(L, blockIdx.x, gridDim.x, threadIdx.x), red);
   if (threadIdx.x == 0) L.h.partials[L.part0 + blockIdx.x] = acc.word();
 }
 
@@ -291,34 +341,34 @@ __device__ __forceinline__ void store_vec(typename Elem<OT>::T* out, const float
   }
 }
 
+// A whole chunk, already loaded, into an output that takes vectors.
 template <int DT, int OT>
-__device__ __forceinline__ void scale_chunk(const GradTensor& T, long long v0, int tid, float s) {
+__device__ __forceinline__ void scale_raw(const GradTensor& T, long long v0, int tid, float s, const Raw& r) {
+  constexpr int E = Elem<DT>::E;
+  typename Elem<OT>::T* out = reinterpret_cast<typename Elem<OT>::T*>(T.out) - T.mis + (v0 + tid) * E;
+#pragma unroll
+  for (int j = 0; j < GRAD_VEC; ++j) {
+    float f[E];
+    Elem<DT>::unpack(r.v[j], f);
+    store_vec<OT, E>(out + j * GRAD_THREADS * E, f, s, T.out_vec > 1);
+  }
+}
+
+template <int DT, int OT>
+__device__ __forceinline__ void scale_ragged(const GradTensor& T, long long v0, int tid, float s) {
   typedef Elem<DT> X;
   typedef Elem<OT> Y;
   constexpr int E = X::E;
-  const typename X::T* g = reinterpret_cast<const typename X::T*>(T.g) - T.mis;   // of vector 0
+  const typename X::T* g = reinterpret_cast<const typename X::T*>(vector0(T));
   typename Y::T* out = reinterpret_cast<typename Y::T*>(T.out) - T.mis;
-  const long long end = T.numel + T.mis;
-  if (T.out_vec && (v0 > 0 || T.mis == 0) && (v0 + GRAD_CHUNK_VECS) * E <= end) {
-    const uint4* p = reinterpret_cast<const uint4*>(g) + v0 + tid;
-    uint4 raw[GRAD_VEC];
-#pragma unroll
-    for (int j = 0; j < GRAD_VEC; ++j) raw[j] = __ldcs(p + j * GRAD_THREADS);
-#pragma unroll
-    for (int j = 0; j < GRAD_VEC; ++j) {
-      float f[E];
-      X::unpack(raw[j], f);
-      store_vec<OT, E>(out + (v0 + tid + j * GRAD_THREADS) * E, f, s, T.out_vec > 1);
-    }
-    return;
-  }
+  const long long end = T.numel + T.mis;   // elements are counted from vector 0 here
   if (T.out_vec) {
     const long long v1 = min(v0 + GRAD_CHUNK_VECS, (end + E - 1) / E);
     for (long long v = v0 + tid; v < v1; v += GRAD_THREADS) {
       const long long e = v * E;
       if (e >= T.mis && e + E <= end) {
         float f[E];
-        X::unpack(__ldcs(reinterpret_cast<const uint4*>(g) + v), f);
+        X::unpack(*(reinterpret_cast<const uint4*>(g) + v), f);
         store_vec<OT, E>(out + e, f, s, T.out_vec > 1);
       } else {
         for (int k = 0; k < E; ++k)
@@ -330,44 +380,73 @@ __device__ __forceinline__ void scale_chunk(const GradTensor& T, long long v0, i
   // The output is not aligned where the input is: single elements, neighbours
   // in neighbouring threads.
   const long long e1 = min((v0 + GRAD_CHUNK_VECS) * E, end);
+#pragma unroll 4
   for (long long e = max(v0 * E, (long long)T.mis) + tid; e < e1; e += GRAD_THREADS)
     out[e] = Y::narrow(__fmul_rn(s, X::widen(g[e])));
 }
 
-template <int DT>
-__device__ __forceinline__ void scale_chunk_to(const GradTensor& T, long long v0, int tid, float s) {
-  if (T.out_dtype == MUON_F32) scale_chunk<DT, MUON_F32>(T, v0, tid, s);
-  else if (T.out_dtype == MUON_BF16) scale_chunk<DT, MUON_BF16>(T, v0, tid, s);
-  else scale_chunk<DT, MUON_F16>(T, v0, tid, s);
+// One chunk; `raw` holds it already if `loaded` (then it is whole and its
+// output takes vectors).
+template <int DT, int OT>
+__device__ __forceinline__ void scale_chunk(const GradTensor& T, long long v0, int tid, float s, bool loaded,
+                                            Raw& raw) {
+  if (!loaded) {
+    if (!T.out_vec || !whole_chunk(T, v0)) {
+      scale_ragged<DT, OT>(T, v0, tid, s);
+      return;
+    }
+    load_chunk<true>(T, v0, tid, raw);
+  }
+  scale_raw<DT, OT>(T, v0, tid, s, raw);
 }
 
-__device__ __forceinline__ void scale_chunk_of(const GradTensor& T, long long v0, int tid, float s) {
+template <int DT>
+__device__ __forceinline__ void scale_chunk_to(const GradTensor& T, long long v0, int tid, float s,
+                                               bool loaded, Raw& raw) {
+  if (T.out_dtype == MUON_F32) scale_chunk<DT, MUON_F32>(T, v0, tid, s, loaded, raw);
+  else if (T.out_dtype == MUON_BF16) scale_chunk<DT, MUON_BF16>(T, v0, tid, s, loaded, raw);
+  else scale_chunk<DT, MUON_F16>(T, v0, tid, s, loaded, raw);
+}
+
+__device__ __forceinline__ void scale_chunk_of(const GradTensor& T, long long v0, int tid, float s,
+                                               bool loaded, Raw& raw) {
   if (s == 1.f && T.out == T.g) return;   // in place and under the bound: 1 * g is g
-  if (T.dtype == MUON_F32) scale_chunk_to<MUON_F32>(T, v0, tid, s);
-  else if (T.dtype == MUON_BF16) scale_chunk_to<MUON_BF16>(T, v0, tid, s);
-  else scale_chunk_to<MUON_F16>(T, v0, tid, s);
+  if (T.dtype == MUON_F32) scale_chunk_to<MUON_F32>(T, v0, tid, s, loaded, raw);
+  else if (T.dtype == MUON_BF16) scale_chunk_to<MUON_BF16>(T, v0, tid, s, loaded, raw);
+  else scale_chunk_to<MUON_F16>(T, v0, tid, s, loaded, raw);
 }
 
 // Chunks are taken from the last to the first: the norm read them in
-// ascending order, so the last ones are the ones still in L2.
+// ascending order, so the last ones are the ones still in L2.  The CTA's first
+// chunk is loaded before the norm is there.
 template <int N>
 __global__ void __launch_bounds__(GRAD_THREADS) grad_scale_kernel(const __grid_constant__ GradLaunch<N> L) {
   __shared__ unsigned long long red[GRAD_THREADS / 32];
+  int c = L.nchunks - 1 - blockIdx.x;
+  int ti = tensor_of(L.chunk0, L.n, c, 0);
+  long long v0 = (long long)(c - L.chunk0[ti]) * GRAD_CHUNK_VECS;
+  Raw raw;
+  bool loaded = L.t[ti].out_vec && whole_chunk(L.t[ti], v0);
+  if (loaded) load_chunk<true>(L.t[ti], v0, threadIdx.x, raw);
   pdl_wait();
   const double norm = joined(L.h, red);
   const float s = scale_of(norm, L.h);
   if (blockIdx.x == 0 && threadIdx.x == 0 && L.h.norm) write_results(L.h, norm, s);
   if (s == 1.f && L.in_place) return;
-  for (int k = blockIdx.x; k < L.nchunks; k += gridDim.x) {
-    const int c = L.nchunks - 1 - k;
-    const int ti = tensor_of(L.chunk0, L.n, c, 0);
-    scale_chunk_of(L.t[ti], (long long)(c - L.chunk0[ti]) * GRAD_CHUNK_VECS, threadIdx.x, s);
+  for (;;) {
+    scale_chunk_of(L.t[ti], v0, threadIdx.x, s, loaded, raw);
+    c -= gridDim.x;
+    if (c < 0) break;
+    if (c < L.chunk0[ti]) ti = tensor_of(L.chunk0, ti, c, 0);
+    v0 = (long long)(c - L.chunk0[ti]) * GRAD_CHUNK_VECS;
+    loaded = false;
   }
 }
 
 // ---------------------------------------------------------------- short lists: one cluster
 // Each CTA is CLUSTER_GROUPS groups of GRAD_THREADS threads; a group takes
-// every (groups of the cluster)-th chunk.
+// every (groups of the cluster)-th chunk, and reads it again to scale it (from
+// L1 or L2: kept in registers it came out no faster).
 constexpr int CLUSTER_GROUPS = GRAD_CLUSTER_THREADS / GRAD_THREADS;
 
 template <int P>
@@ -380,13 +459,7 @@ __global__ void __launch_bounds__(GRAD_CLUSTER_THREADS, 1)
   asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");   // this CTA has started
   const int tid = threadIdx.x % GRAD_THREADS;
   const int group = rank * CLUSTER_GROUPS + threadIdx.x / GRAD_THREADS, groups = ctas * CLUSTER_GROUPS;
-  Acc<P> acc;
-  int ti = 0;
-  for (int c = group; c < L.nchunks; c += groups) {
-    ti = tensor_of(L.chunk0, L.n, c, ti);
-    norm_chunk_of<P>(L.t[ti], (long long)(c - L.chunk0[ti]) * GRAD_CHUNK_VECS, tid, acc);
-  }
-  acc = block_join<P, GRAD_CLUSTER_THREADS>(acc, red);
+  const Acc<P> acc = block_join<P, GRAD_CLUSTER_THREADS>(add_chunks<P>(L, group, groups, tid), red);
   asm volatile("barrier.cluster.wait.aligned;" ::: "memory");             // every CTA has
   if (threadIdx.x < ctas) *cluster.map_shared_rank(&all[rank], threadIdx.x) = acc.word();
   cluster.sync();   // every CTA's value is in every CTA's `all`
@@ -399,11 +472,12 @@ __global__ void __launch_bounds__(GRAD_CLUSTER_THREADS, 1)
   const double norm = sum.norm();
   const float s = scale_of(norm, L.h);
   if (rank == 0 && threadIdx.x == 0) write_results(L.h, norm, s);
-  if (!L.scales) return;
-  ti = 0;
+  if (!L.scales || (s == 1.f && L.in_place)) return;
+  int ti = 0;
   for (int c = group; c < L.nchunks; c += groups) {
     ti = tensor_of(L.chunk0, L.n, c, ti);
-    scale_chunk_of(L.t[ti], (long long)(c - L.chunk0[ti]) * GRAD_CHUNK_VECS, tid, s);
+    Raw raw;
+    scale_chunk_of(L.t[ti], (long long)(c - L.chunk0[ti]) * GRAD_CHUNK_VECS, tid, s, false, raw);
   }
 }
 

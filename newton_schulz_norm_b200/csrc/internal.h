@@ -241,12 +241,22 @@ struct AdamWLaunch {
 constexpr int GRAD_THREADS = 256;
 constexpr int GRAD_VEC = 4;                                    // vectors per thread and chunk
 constexpr int GRAD_CHUNK_VECS = GRAD_THREADS * GRAD_VEC;       // 16 KB
+constexpr int GRAD_CHUNK_SHIFT = 10;                           // log2 of it
+static_assert(GRAD_CHUNK_VECS == 1 << GRAD_CHUNK_SHIFT, "chunk counts are shifts");
 constexpr int GRAD_MAX_TENSORS = 512;                          // per launch
 constexpr int GRAD_SHORT_TENSORS = 64;                         // per launch with the short table
+// CTAs of the partial launch on each SM, of the 8 that fit.  The list of GPT-2
+// 124M in bf16 (249 MB) takes 47.7, 47.5, 46.5, 45.6 us with 5, 6, 7, 8 of them, the
+// largest (6.2 GB fp32) 887, 871, 871, 904 us.
+constexpr int GRAD_PARTIAL_CTAS = 7;
 constexpr int GRAD_MAX_CTAS = 148 * 8;                         // partial values of one launch
+// Of a list that is scaled, the part that the norm's reading leaves in L2: 64
+// MB.  Clipping GPT-2 124M (bf16 into fp32; fp32 in place) takes 174 and 250 us
+// without this, 170 and 240 us with 64 MB, 171 and 247 us with 96 MB.
+constexpr int GRAD_KEEP_CHUNKS = 4096;
 // Lists of at most GRAD_CLUSTER_CHUNKS chunks take the one-cluster kernel.
 constexpr int GRAD_CLUSTER_CHUNKS = GRAD_SHORT_TENSORS;        // 1 MB
-constexpr int GRAD_CLUSTER_THREADS = 1024;
+constexpr int GRAD_CLUSTER_THREADS = 512;
 constexpr int GRAD_CLUSTER_MAX = 8;                            // CTAs
 
 enum GradNorm : int { GRAD_L1 = 1, GRAD_L2 = 2, GRAD_INF = 3 };
@@ -282,7 +292,7 @@ struct GradLaunch {
   int nchunks;               // chunks of all of them
   int part0;                 // first partial value this launch writes
   int in_place;              // every out is its g
-  int scales;                // one-cluster kernel: scale as well
+  int scales;                // the call scales the gradients as well
   int chunk0[N];             // first chunk of each tensor in the launch
   GradTensor t[N];
 };

@@ -24,13 +24,21 @@
 // pass-1 item of their matrix, so a waiting CTA only ever waits on CTAs that
 // have claimed work ahead of it; the wait is still bounded and reports
 // MUON_ERR_TIMEOUT instead of hanging.
+//
+// A gradient scale (clipping) is one multiplication on the way in, in both
+// passes; 245 us with it and without on the 48 matrices of GPT-2 124M, of
+// which the 14 bytes an element cannot do without take 182 us at the copy
+// rate.  What u is made of (plain, momentum, Nesterov) and whether a tile is
+// whole are template arguments: with both decided per element the same
+// launch took 260 us, and the four matrices of one block 37.6 instead of
+// 31.7 us.  Ragged tiles load a group of elements before they use the first:
+// three matrices with odd sides (129 x 1001 and the like) 24 instead of 48 us.
 #include "internal.h"
 #include "ptx.cuh"
 
 namespace muon {
 
 namespace {
-
 
 // L2 residency hints.  Pass 1 loads g and buf and stores buf with an
 // evict-last policy: pass 2 of the same matrix reads them again a few
@@ -90,64 +98,100 @@ __device__ __forceinline__ float taken(float g, float s) {
   return SCALED ? __fmul_rn(s, g) : g;
 }
 
-__device__ __forceinline__ float momentum_u(float g, float& b, float beta, int mode, int nesterov) {
-  if (mode == K1_PLAIN) return g;
+// What u is made of.
+enum Rule : int { RULE_PLAIN, RULE_MOMENTUM, RULE_NESTEROV };
+
+template <int RULE>
+__device__ __forceinline__ float momentum_u(float g, float& b, float beta) {
+  if (RULE == RULE_PLAIN) return g;
   b = fmaf(beta, b, g);
-  return nesterov ? fmaf(beta, b, g) : b;
+  return RULE == RULE_NESTEROV ? fmaf(beta, b, g) : b;
 }
 
-__device__ __forceinline__ float u_from(float g, float bnew, float beta, int mode, int nesterov) {
-  if (mode == K1_PLAIN) return g;
-  return nesterov ? fmaf(beta, bnew, g) : bnew;
+template <int RULE>
+__device__ __forceinline__ float u_from(float g, float bnew, float beta) {
+  if (RULE == RULE_PLAIN) return g;
+  return RULE == RULE_NESTEROV ? fmaf(beta, bnew, g) : bnew;
+}
+
+// The thread's four runs of four columns of one 64 x 64 tile (rows lrow + 16 k),
+// all loaded before any is used.  WHOLE: the tile lies inside the matrix and
+// its rows are 16-byte aligned (c a multiple of 4).  Otherwise the elements are
+// loaded one by one, those outside as zero, RAGGED_RUNS runs at a time: all
+// four at once would cost the whole tiles registers.
+struct Runs {
+  float4 g[4], b[4];
+};
+constexpr int RAGGED_RUNS = 2;
+
+template <int RULE, bool WHOLE>
+__device__ __forceinline__ void load_runs(const K1Ptrs& P, long long r, long long c, long long gr0,
+                                          long long gc, uint64_t pol, Runs& R) {
+#pragma unroll
+  for (int k = 0; k < (WHOLE ? 4 : RAGGED_RUNS); ++k) {
+    const long long gr = gr0 + 16 * k;
+    const long long off = gr * c + gc;
+    R.g[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    R.b[k] = R.g[k];
+    if (WHOLE) {
+      R.g[k] = ld_hint(P.g + off, pol);
+      if (RULE != RULE_PLAIN) R.b[k] = ld_hint(P.buf + off, pol);
+    } else {
+      const bool row = gr < r, has_buf = RULE != RULE_PLAIN;
+      if (row && gc < c) R.g[k].x = P.g[off];
+      if (row && gc + 1 < c) R.g[k].y = P.g[off + 1];
+      if (row && gc + 2 < c) R.g[k].z = P.g[off + 2];
+      if (row && gc + 3 < c) R.g[k].w = P.g[off + 3];
+      if (row && has_buf && gc < c) R.b[k].x = __ldcg(P.buf + off);
+      if (row && has_buf && gc + 1 < c) R.b[k].y = __ldcg(P.buf + off + 1);
+      if (row && has_buf && gc + 2 < c) R.b[k].z = __ldcg(P.buf + off + 2);
+      if (row && has_buf && gc + 3 < c) R.b[k].w = __ldcg(P.buf + off + 3);
+    }
+  }
+}
+
+__device__ __forceinline__ bool whole_tile(const K1Info& q, long long r0, long long c0) {
+  return (q.c & 3) == 0 && r0 + K1_TILE <= q.r && c0 + K1_TILE <= q.c;
 }
 
 // Pass 1 on one 64 x 64 tile: momentum (buf written back) and this thread's
-// sum of squares of u.  Every load of the thread is issued before any store.
-template <bool SCALED>
+// sum of squares of u.  A run of four whole aligned columns sums its squares in
+// fp32 first, in ragged tiles too.
+template <int RULE, bool SCALED, bool WHOLE>
 __device__ __forceinline__ double pass1_tile(const K1Launch& L, const K1Ptrs& P, long long r,
                                              long long c, long long r0, long long c0, int lrow,
                                              int lcol, float s, uint64_t pol) {
-  const bool vec = (c & 3) == 0;
-  const float beta = L.beta;
+  const long long gc = c0 + lcol;
+  constexpr int RUNS = WHOLE ? 4 : RAGGED_RUNS;
   double ss = 0.0;
-  float4 g4[4], b4[4];
-  bool full[4];
+#pragma unroll 1
+  for (int k0 = 0; k0 < 4; k0 += RUNS) {
+    Runs R;
+    load_runs<RULE, WHOLE>(P, r, c, r0 + lrow + 16 * k0, gc, pol, R);
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const long long gr = r0 + lrow + 16 * k;
-    const long long gc = c0 + lcol;
-    full[k] = vec && gr < r && gc + 4 <= c;
-    g4[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-    b4[k] = g4[k];
-    if (full[k]) {
-      const long long off = gr * c + gc;
-      g4[k] = ld_hint(P.g + off, pol);
-      if (L.mode != K1_PLAIN) b4[k] = ld_hint(P.buf + off, pol);
-    }
-  }
+    for (int k = 0; k < RUNS; ++k) {
+      const long long gr = r0 + lrow + 16 * (k0 + k);
+      const float gv[4] = {R.g[k].x, R.g[k].y, R.g[k].z, R.g[k].w};
+      float bv[4] = {R.b[k].x, R.b[k].y, R.b[k].z, R.b[k].w};
+      float u[4];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const long long gr = r0 + lrow + 16 * k;
-    const long long gc = c0 + lcol;
-    if (full[k]) {
-      float gv[4] = {g4[k].x, g4[k].y, g4[k].z, g4[k].w};
-      float bv[4] = {b4[k].x, b4[k].y, b4[k].z, b4[k].w};
-      float sq = 0.f;
+      for (int e = 0; e < 4; ++e) u[e] = momentum_u<RULE>(taken<SCALED>(gv[e], s), bv[e], L.beta);
+      if (WHOLE || ((c & 3) == 0 && gr < r && gc + 4 <= c)) {
+        float sq = 0.f;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float u = momentum_u(taken<SCALED>(gv[e], s), bv[e], beta, L.mode, L.nesterov);
-        sq = fmaf(u, u, sq);
-      }
-      ss += (double)sq;
-      if (L.mode != K1_PLAIN)
-        st_hint(P.buf + gr * c + gc, make_float4(bv[0], bv[1], bv[2], bv[3]), pol);
-    } else if (gr < r && gc < c) {
-      const long long off = gr * c + gc;
-      for (int e = 0; e < 4 && gc + e < c; ++e) {
-        float b = (L.mode != K1_PLAIN) ? P.buf[off + e] : 0.f;
-        const float u = momentum_u(taken<SCALED>(P.g[off + e], s), b, beta, L.mode, L.nesterov);
-        ss += (double)u * (double)u;
-        if (L.mode != K1_PLAIN) P.buf[off + e] = b;
+        for (int e = 0; e < 4; ++e) sq = fmaf(u[e], u[e], sq);
+        ss += (double)sq;
+        if (RULE != RULE_PLAIN)
+          st_hint(P.buf + gr * c + gc, make_float4(bv[0], bv[1], bv[2], bv[3]), pol);
+      } else if (gr < r) {
+        const long long off = gr * c + gc;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (gc + e < c) {
+            ss += (double)u[e] * (double)u[e];
+            if (RULE != RULE_PLAIN) P.buf[off + e] = bv[e];
+          }
+        }
       }
     }
   }
@@ -156,68 +200,48 @@ __device__ __forceinline__ double pass1_tile(const K1Launch& L, const K1Ptrs& P,
 
 // Pass 2 on one 64 x 64 tile: recompute u from g and the new buf, scale by
 // 1/(norm + eps) in double, round once to bf16 and store oriented.
-template <bool SCALED>
+template <int RULE, bool SCALED, bool WHOLE>
 __device__ __forceinline__ void pass2_tile(const K1Launch& L, const K1Ptrs& P, const K1Info& info,
                                            long long r0, long long c0, double inv, int tid,
                                            int lrow, int lcol, uint16_t (*s_tile)[K1_TILE + 2],
                                            float s, uint64_t pol) {
   const long long r = info.r, c = info.c;
-  const bool vec = (c & 3) == 0;
-  const float beta = L.beta;
   const bool tr = info.transposed != 0;
-  float4 g4[4], b4[4];
-  bool full[4];
+  constexpr int RUNS = WHOLE ? 4 : RAGGED_RUNS;
+#pragma unroll 1
+  for (int k0 = 0; k0 < 4; k0 += RUNS) {
+    Runs R;
+    load_runs<RULE, WHOLE>(P, r, c, r0 + lrow + 16 * k0, c0 + lcol, pol, R);
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const long long gr = r0 + lrow + 16 * k;
-    const long long gc = c0 + lcol;
-    full[k] = vec && gr < r && gc + 4 <= c;
-    g4[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-    b4[k] = g4[k];
-    if (full[k]) {
-      const long long off = gr * c + gc;
-      g4[k] = ld_hint(P.g + off, pol);
-      if (L.mode != K1_PLAIN) b4[k] = ld_hint(P.buf + off, pol);
-    }
-  }
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int row = lrow + 16 * k;
-    const long long gr = r0 + row;
-    const long long gc = c0 + lcol;
-    uint16_t bits[4] = {0, 0, 0, 0};
-    if (gr < r && gc < c) {
-      const long long off = gr * c + gc;
-      if (full[k]) {
-        const float gv[4] = {g4[k].x, g4[k].y, g4[k].z, g4[k].w};
-        const float bv[4] = {b4[k].x, b4[k].y, b4[k].z, b4[k].w};
+    for (int k = 0; k < RUNS; ++k) {
+      const int row = lrow + 16 * (k0 + k);
+      const long long gr = r0 + row;
+      const long long gc = c0 + lcol;
+      uint16_t bits[4] = {0, 0, 0, 0};
+      if (gr < r && gc < c) {
+        const float gv[4] = {R.g[k].x, R.g[k].y, R.g[k].z, R.g[k].w};
+        const float bv[4] = {R.b[k].x, R.b[k].y, R.b[k].z, R.b[k].w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float u = u_from(taken<SCALED>(gv[e], s), bv[e], beta, L.mode, L.nesterov);
+          const float u = u_from<RULE>(taken<SCALED>(gv[e], s), bv[e], L.beta);
           bits[e] = __bfloat16_as_ushort(__double2bfloat16((double)u * inv));
         }
-      } else {
-        for (int e = 0; e < 4 && gc + e < c; ++e) {
-          const float b = (L.mode != K1_PLAIN) ? __ldcg(P.buf + off + e) : 0.f;
-          const float u = u_from(taken<SCALED>(P.g[off + e], s), b, beta, L.mode, L.nesterov);
-          bits[e] = __bfloat16_as_ushort(__double2bfloat16((double)u * inv));
+        if (!tr) {
+          __nv_bfloat16* dst = P.x0 + gr * info.ldx + gc;
+          if (gc + 4 <= c) {
+            uint2 w;
+            w.x = (uint32_t)bits[0] | ((uint32_t)bits[1] << 16);
+            w.y = (uint32_t)bits[2] | ((uint32_t)bits[3] << 16);
+            st_hint_u2(dst, w, pol);
+          } else {
+            for (int e = 0; e < 4 && gc + e < c; ++e) dst[e] = __ushort_as_bfloat16(bits[e]);
+          }
         }
       }
-      if (!tr) {
-        __nv_bfloat16* dst = P.x0 + gr * info.ldx + gc;
-        if (gc + 4 <= c) {
-          uint2 w;
-          w.x = (uint32_t)bits[0] | ((uint32_t)bits[1] << 16);
-          w.y = (uint32_t)bits[2] | ((uint32_t)bits[3] << 16);
-          st_hint_u2(dst, w, pol);
-        } else {
-          for (int e = 0; e < 4 && gc + e < c; ++e) dst[e] = __ushort_as_bfloat16(bits[e]);
-        }
-      }
-    }
-    if (tr) {
+      if (tr) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s_tile[row][lcol + e] = bits[e];
+        for (int e = 0; e < 4; ++e) s_tile[row][lcol + e] = bits[e];
+      }
     }
   }
   if (tr) {
@@ -246,7 +270,7 @@ __device__ __forceinline__ void pass2_tile(const K1Launch& L, const K1Ptrs& P, c
   }
 }
 
-template <bool SCALED>
+template <int RULE, bool SCALED>
 __global__ void __launch_bounds__(K1_THREADS, 4) k1_kernel(const __grid_constant__ K1Launch L) {
   __shared__ int s_item;
   __shared__ int s_flag;
@@ -294,7 +318,9 @@ __global__ void __launch_bounds__(K1_THREADS, 4) k1_kernel(const __grid_constant
       for (int t = t0; t < t1; ++t) {
         const long long r0 = (long long)(t / info.tiles_c) * K1_TILE;
         const long long c0 = (long long)(t % info.tiles_c) * K1_TILE;
-        ss += pass1_tile<SCALED>(L, P, info.r, info.c, r0, c0, lrow, lcol, s, pol_keep);
+        ss += whole_tile(info, r0, c0)
+                  ? pass1_tile<RULE, SCALED, true>(L, P, info.r, info.c, r0, c0, lrow, lcol, s, pol_keep)
+                  : pass1_tile<RULE, SCALED, false>(L, P, info.r, info.c, r0, c0, lrow, lcol, s, pol_keep);
       }
       const double tot = block_sum(ss, s_red);
       if (tid == 0) {
@@ -341,7 +367,10 @@ __global__ void __launch_bounds__(K1_THREADS, 4) k1_kernel(const __grid_constant
     for (int t = t0; t < t1; ++t) {
       const long long r0 = (long long)(t / info.tiles_c) * K1_TILE;
       const long long c0 = (long long)(t % info.tiles_c) * K1_TILE;
-      pass2_tile<SCALED>(L, P, info, r0, c0, inv, tid, lrow, lcol, s_tile, s, pol_drop);
+      if (whole_tile(info, r0, c0))
+        pass2_tile<RULE, SCALED, true>(L, P, info, r0, c0, inv, tid, lrow, lcol, s_tile, s, pol_drop);
+      else
+        pass2_tile<RULE, SCALED, false>(L, P, info, r0, c0, inv, tid, lrow, lcol, s_tile, s, pol_drop);
     }
   }
 }
@@ -369,19 +398,33 @@ __global__ void apply_kernel(const __grid_constant__ ApplyLaunch L) {
   }
 }
 
+typedef void (*K1Kernel)(const K1Launch);
+
+K1Kernel k1_kernel_for(int mode, int nesterov, bool scaled) {
+  if (mode == K1_PLAIN) return k1_kernel<RULE_PLAIN, false>;
+  if (nesterov) return scaled ? k1_kernel<RULE_NESTEROV, true> : k1_kernel<RULE_NESTEROV, false>;
+  return scaled ? k1_kernel<RULE_MOMENTUM, true> : k1_kernel<RULE_MOMENTUM, false>;
+}
+
 }  // namespace
 
 int k1_blocks_per_sm() {
-  int n = 0;
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k1_kernel<false>, K1_THREADS, 0) != cudaSuccess || n < 1)
-    return 1;
-  return n;
+  int least = 0;
+  for (int k = 0; k < 5; ++k) {
+    int n = 0;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(
+            &n, k1_kernel_for(k == 4 ? K1_PLAIN : K1_MOMENTUM, k & 1, (k & 2) != 0), K1_THREADS, 0) !=
+            cudaSuccess ||
+        n < 1)
+      return 1;
+    least = k == 0 || n < least ? n : least;
+  }
+  return least;
 }
 
 cudaError_t launch_k1(const K1Launch& L, int grid, cudaStream_t stream) {
   if (L.nitems <= 0) return cudaSuccess;
-  if (L.grad_scale) k1_kernel<true><<<grid, K1_THREADS, 0, stream>>>(L);
-  else k1_kernel<false><<<grid, K1_THREADS, 0, stream>>>(L);
+  k1_kernel_for(L.mode, L.nesterov, L.grad_scale != nullptr)<<<grid, K1_THREADS, 0, stream>>>(L);
   return cudaGetLastError();
 }
 

@@ -1010,7 +1010,8 @@ int dtype_size(int dtype) { return dtype == MUON_F32 ? 4 : 2; }
 // Chunks of one tensor; a tensor that starts off a 16-byte boundary may touch
 // one vector more than its length alone would.
 long long grad_chunks(long long numel, int mis, int dtype) {
-  return cdiv(cdiv(numel + mis, 16 / dtype_size(dtype)), GRAD_CHUNK_VECS);
+  const int shift = GRAD_CHUNK_SHIFT + (dtype == MUON_F32 ? 2 : 3);   // log2 of a chunk's elements
+  return (numel + mis + (1ll << shift) - 1) >> shift;
 }
 
 int grad_norm_of(double p) {
@@ -1048,7 +1049,7 @@ int check_grad_list(const void* const* ptrs, const unsigned char* dtypes, const 
     if (numels[i] < 0 || numels[i] > kGradMaxNumel || dtypes[i] > MUON_F16) return MUON_ERR_INVALID_ARG;
     if (numels[i] == 0) continue;
     if (!ptrs[i]) return MUON_ERR_INVALID_ARG;
-    if (reinterpret_cast<uintptr_t>(ptrs[i]) % dtype_size(dtypes[i])) return MUON_ERR_UNSUPPORTED;
+    if (reinterpret_cast<uintptr_t>(ptrs[i]) & (dtype_size(dtypes[i]) - 1)) return MUON_ERR_UNSUPPORTED;
   }
   return MUON_OK;
 }
@@ -1064,7 +1065,7 @@ struct GradList {
 };
 
 int grad_mis(const GradList& a, int i) {
-  return (int)((reinterpret_cast<uintptr_t>(a.grads[i]) & 15u) / dtype_size(a.dtypes[i]));
+  return (int)(reinterpret_cast<uintptr_t>(a.grads[i]) & 15u) >> (a.dtypes[i] == MUON_F32 ? 2 : 1);
 }
 
 GradTensor grad_tensor(const GradList& a, int i) {
@@ -1077,7 +1078,7 @@ GradTensor grad_tensor(const GradList& a, int i) {
   T.mis = (unsigned char)grad_mis(a, i);
   const int size = dtype_size(T.out_dtype), bytes = 16 / dtype_size(T.dtype) * size;   // of a vector's worth
   const uintptr_t at = reinterpret_cast<uintptr_t>(T.out) - (uintptr_t)(T.mis * size);
-  T.out_vec = at % std::min(16, bytes) ? 0 : bytes == 32 && at % 32 == 0 ? 2 : 1;
+  T.out_vec = at & (std::min(16, bytes) - 1) ? 0 : bytes == 32 && at % 32 == 0 ? 2 : 1;
   return T;
 }
 
@@ -1112,8 +1113,8 @@ int run_grad_long(DeviceCtx* ctx, const GradList& a, const GradCall& call, cudaS
   static thread_local GradLaunch<N> L;
   L.h = call;
   L.h.npartials = 0;
-  L.scales = 0;
-  const int most = std::min(GRAD_MAX_CTAS, ctx->num_sms * ctx->grad_blocks_per_sm);
+  L.scales = a.outs != nullptr;
+  const int most = std::min(GRAD_MAX_CTAS, ctx->num_sms * std::min(GRAD_PARTIAL_CTAS, ctx->grad_blocks_per_sm));
   int rc = grad_walk(a, L, [&]() -> int {
     const int grid = std::min(L.nchunks, most);
     L.part0 = L.h.npartials;
