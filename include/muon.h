@@ -234,8 +234,9 @@ MUON_API int muon_momentum_normalize_noalloc(const float* const* grads, float* c
  *           1/sqrt(1-beta2^t), 1-lr*lambda_i) are formed in double on the host
  *           and rounded once to fp32; the per-element arithmetic is fp32.
  *   stream  cudaStream_t as void*.
- * Pointers need only be 4-byte aligned: tensors whose four pointers are all
- * 16-byte aligned take 16-byte vector accesses, the others scalar ones.
+ * Pointers need only be 4-byte aligned: tensors whose four pointers are equally
+ * far past a 16-byte boundary take 16-byte vector accesses, the others scalar
+ * ones.
  * Tensors must not alias one another.  NaN/Inf stay in the elements they
  * reach.  One kernel launch per 128 tensors; nothing is allocated.
  */

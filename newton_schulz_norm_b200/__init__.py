@@ -89,7 +89,7 @@ def library() -> ctypes.CDLL:
         "muon_grad_norm": (i, [_P, _P, _P, i, d, d, d, _P, _P, _P, i64, _P]),
         "muon_clip_grads": (i, [_P, _P, _P, i, _P, _P, d, d, d, _P, _P, _P, i64, _P]),
         "muon_step_scaled": (i, [_PP, _PP, _PP, _I64P, i, f, f, i, i, _FP, _PP, i, _P, _P]),
-        "muon_adamw_step_scaled": (i, [_PP, _PP, _PP, _PP, _I64P, _P, i, i64, d, d, d, d, d, _P, _P]),
+        "muon_adamw_step_scaled": (i, [_P, _P, _P, _P, _P, _P, i, i64, d, d, d, d, d, _P, _P]),
         "muon_momentum_normalize_scaled": (i, [_PP, _PP, _PP, _I64P, _I64P, i, f, i, _P, _P]),
     }
     for name, (res, args) in sig.items():
@@ -331,15 +331,16 @@ class AdamWGroup:
             (ctypes.c_ubyte * max(n, 1))(*[1 if d else 0 for d in decay])
         self.lr, self.betas, self.eps, self.weight_decay = float(lr), tuple(betas), float(eps), \
             float(weight_decay)
+        at = ctypes.addressof
+        self._args = (at(self._p), at(self._g), at(self._m), at(self._v), at(self._numels),
+                      None if self._decay is None else at(self._decay), n)
 
     def step(self, step: int, lr: float | None = None, stream=None,
              grad_scale: torch.Tensor | None = None) -> None:
         """One AdamW step (t = ``step``, from 1) on the group's tensors;
         ``grad_scale`` as for adamw_step."""
         code = library().muon_adamw_step_scaled(
-            self._p, self._g, self._m, self._v, self._numels,
-            ctypes.cast(self._decay, ctypes.c_void_p) if self._decay is not None else None,
-            self._n, int(step), self.lr if lr is None else float(lr), float(self.betas[0]),
+            *self._args, int(step), self.lr if lr is None else float(lr), float(self.betas[0]),
             float(self.betas[1]), self.eps, self.weight_decay, _scale_ptr(grad_scale),
             _stream_ptr(stream))
         _check(code, "muon_adamw_step")

@@ -149,19 +149,6 @@ __device__ __forceinline__ Acc<P> block_join(Acc<P> a, unsigned long long* red) 
 // [v E - mis, (v + 1) E - mis).  Only the first and the last can be partial;
 // those are read element by element, so nothing outside the tensor is touched.
 
-// The tensor that holds chunk c, from lo on (chunk0 ascends): mostly the one
-// that held the last chunk.
-__device__ __forceinline__ int tensor_of(const int* chunk0, int n, int c, int lo) {
-  int hi = n;
-  if (lo + 1 >= n || chunk0[lo + 1] > c) return lo;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (chunk0[mid] <= c) lo = mid;
-    else hi = mid;
-  }
-  return lo;
-}
-
 // Whether chunk v0.. of the tensor is nothing but whole vectors.
 __device__ __forceinline__ bool whole_chunk(const GradTensor& T, long long v0) {
   const int shift = T.dtype == MUON_F32 ? 2 : 3;   // log2 of a vector's elements

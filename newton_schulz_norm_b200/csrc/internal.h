@@ -144,7 +144,7 @@ struct NsLaunch {
 // 64 x 64 tiles of the stored matrix, in two passes joined per matrix.
 constexpr int K1_TILE = 64;
 constexpr int K1_THREADS = 256;
-constexpr int K1_GROUP = 4;  // 64x64 tiles per work item (one norm partial, one fence)
+constexpr int K1_GROUP = 4;  // most 64x64 tiles per work item (one norm partial, one fence)
 
 enum K1Mode : int { K1_MOMENTUM = 0, K1_PLAIN = 1 };
 
@@ -153,7 +153,8 @@ struct K1Info {              // static per matrix (device memory)
   long long ldx;             // leading dimension of the oriented bf16 X0
   int tiles_c;               // tiles along the stored columns
   int ntiles;                // tiles of this matrix
-  int nitems;                // work items of this matrix (groups of K1_GROUP tiles)
+  int group;                 // tiles per work item, at most K1_GROUP
+  int nitems;                // work items of this matrix
   int part0;                 // offset of its partial sums (one per item)
   int transposed;            // r > c
 };
@@ -165,10 +166,10 @@ struct K1Ptrs {              // per call
 };
 
 // Work item: a matrix (K1_PASS2 set for its second pass) and a group of
-// K1_GROUP consecutive tiles of it.
+// consecutive tiles of it.
 struct K1Item {
   int mat;                   // matrix index; pass 2 items have mat | 0x40000000
-  int group;                 // tiles [group * K1_GROUP, +K1_GROUP) of the matrix
+  int group;                 // tiles [group * info.group, +info.group) of the matrix
 };
 constexpr int K1_PASS2 = 0x40000000;
 
@@ -211,16 +212,30 @@ constexpr int ADAMW_VEC = 2;                                   // float4 per arr
 constexpr int ADAMW_CHUNK = ADAMW_THREADS * ADAMW_VEC * 4;     // 2048 elements
 constexpr int ADAMW_MAX_TENSORS = 128;                         // per launch
 
+// The entry that holds chunk c of a launch's table, from lo on (chunk0
+// ascends): mostly the one that held the last chunk, else by halving.  The
+// first entries are kept apart from the rest of the table so that a search in
+// cold argument memory touches few lines.
+__device__ __forceinline__ int tensor_of(const int* chunk0, int n, int c, int lo) {
+  int hi = n;
+  if (lo + 1 >= n || chunk0[lo + 1] > c) return lo;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (chunk0[mid] <= c) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
 struct AdamWTensor {
   float* p;
   const float* g;
   float* m;                  // running average of the gradient
   float* v;                  // running average of its square
   long long numel;           // > 0
-  int chunk0;                // first chunk of this tensor in the launch
-  int vec;                   // all four pointers 16-byte aligned: float4 path
+  unsigned char vec;         // the four pointers are equally far past a 16-byte boundary
+  unsigned char mis;         // ... by this many elements
   float decay;               // fp32(1 - lr * weight_decay_i)
-  int pad_;
 };
 
 struct AdamWLaunch {
@@ -232,6 +247,7 @@ struct AdamWLaunch {
   float inv_sqrt_bc2;        // fp32(1 / sqrt(1 - beta2^t))
   float eps;
   const float* grad_scale;   // device scalar that multiplies every gradient, or nullptr
+  int chunk0[ADAMW_MAX_TENSORS];   // first chunk of each tensor in the launch
   AdamWTensor t[ADAMW_MAX_TENSORS];
 };
 

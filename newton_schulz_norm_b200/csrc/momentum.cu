@@ -310,8 +310,8 @@ __global__ void __launch_bounds__(K1_THREADS, 4) k1_kernel(const __grid_constant
     }
     const K1Info info = L.info[mat];
     const K1Ptrs P = L.ptrs[mat];
-    const int t0 = item.group * K1_GROUP;
-    const int t1 = min(t0 + K1_GROUP, info.ntiles);
+    const int t0 = item.group * info.group;
+    const int t1 = min(t0 + info.group, info.ntiles);
 
     if (!pass2) {
       double ss = 0.0;

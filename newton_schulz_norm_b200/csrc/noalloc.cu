@@ -181,6 +181,7 @@ extern "C" int muon_momentum_normalize_noalloc(const float* const* grads, float*
     k.ldx = x0_ld[i];
     k.tiles_c = (int)cdiv_ll(c, K1_TILE);
     k.ntiles = (int)(cdiv_ll(r, K1_TILE) * k.tiles_c);
+    k.group = K1_GROUP;
     k.nitems = (int)cdiv_ll(k.ntiles, K1_GROUP);
     k.part0 = (int)items;
     k.transposed = r > c;

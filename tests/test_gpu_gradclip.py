@@ -406,6 +406,33 @@ def test_adamw_scaled_against_the_oracle(muon):
             assert np.all(np.abs(got.cpu().numpy() - ref.astype(np.float64)) <= 2 * bound)
 
 
+@pytest.mark.parametrize("offs", [(0, 0, 0, 0), (1, 1, 1, 1), (3, 3, 3, 3), (0, 1, 0, 0), (2, 1, 3, 0)],
+                         ids=["aligned", "off1", "off3", "grad_off", "all_differ"])
+def test_adamw_at_every_alignment(muon, offs):
+    """Views equally far past a 16-byte boundary take vectors, others single
+    elements; both give the aligned tensors' bits and touch nothing outside."""
+    rng = np.random.default_rng(67)
+    sizes = [1, 2, 3, 4, 5, 7, 8, 2044, 2045, 2047, 2048, 2049, 2051, 4096, 10001]
+    decay = [i % 2 == 0 for i in range(len(sizes))]
+    host = [[rng.standard_normal(n).astype(np.float32) for n in sizes] for _ in range(4)]
+    host[3] = [np.abs(x) for x in host[3]]
+    s = torch.tensor(0.7, device="cuda")
+    want = [_dev(x) for x in host]
+    muon.adamw_step(*want, 3, 1e-2, decay=decay, grad_scale=s)
+    views, bases = [], []
+    for rows, off in zip(host, offs):
+        views.append([])
+        for x in rows:
+            base = torch.full((x.size + 16,), 7.0, device="cuda")
+            base[off:off + x.size] = torch.from_numpy(x).cuda()
+            views[-1].append(base[off:off + x.size])
+            bases.append((base, off, x.size))
+    muon.adamw_step(*views, 3, 1e-2, decay=decay, grad_scale=s)
+    for a, b in zip(sum(want, []), sum(views, [])):
+        assert torch.equal(a, b)
+    _guards_hold(bases)
+
+
 SHAPES = [(256, 256), (129, 257), (300, 7), (7, 300), (1, 1), (1000, 96), (64, 4)]
 
 
