@@ -255,25 +255,31 @@ struct AdamWLaunch {
 // Every tensor is cut into chunks of GRAD_CHUNK_VECS 16-byte vectors;
 // persistent CTAs take chunks in grid-stride order.
 constexpr int GRAD_THREADS = 256;
-constexpr int GRAD_VEC = 4;                                    // vectors per thread and chunk
-constexpr int GRAD_CHUNK_VECS = GRAD_THREADS * GRAD_VEC;       // 16 KB
-constexpr int GRAD_CHUNK_SHIFT = 10;                           // log2 of it
+// Vectors per thread and chunk.  With 8 five CTAs fit an SM, with 4 eight.
+// GPT-2 124M in bf16 (249 MB) takes 44.1 us against 45.3 (seven CTAs: 46.7),
+// GPT-2 medium in fp32 (1.4 GB) 203 against 207 (209), the largest list (6.2 GB) 903
+// against 874 (861); where the memory runs slower, 45.8, 208, 904 against 48.3, 227,
+// 911 with seven CTAs.
+constexpr int GRAD_VEC = 8;
+constexpr int GRAD_CHUNK_VECS = GRAD_THREADS * GRAD_VEC;       // 32 KB
+constexpr int GRAD_CHUNK_SHIFT = 11;                           // log2 of it
 static_assert(GRAD_CHUNK_VECS == 1 << GRAD_CHUNK_SHIFT, "chunk counts are shifts");
 constexpr int GRAD_MAX_TENSORS = 512;                          // per launch
 constexpr int GRAD_SHORT_TENSORS = 64;                         // per launch with the short table
-// CTAs of the partial launch on each SM, of the 8 that fit.  The list of GPT-2
-// 124M in bf16 (249 MB) takes 47.7, 47.5, 46.5, 45.6 us with 5, 6, 7, 8 of them, the
-// largest (6.2 GB fp32) 887, 871, 871, 904 us.
-constexpr int GRAD_PARTIAL_CTAS = 7;
 constexpr int GRAD_MAX_CTAS = 148 * 8;                         // partial values of one launch
 // Of a list that is scaled, the part that the norm's reading leaves in L2: 64
 // MB.  Clipping GPT-2 124M (bf16 into fp32; fp32 in place) takes 174 and 250 us
 // without this, 170 and 240 us with 64 MB, 171 and 247 us with 96 MB.
-constexpr int GRAD_KEEP_CHUNKS = 4096;
-// Lists of at most GRAD_CLUSTER_CHUNKS chunks take the one-cluster kernel.
-constexpr int GRAD_CLUSTER_CHUNKS = GRAD_SHORT_TENSORS;        // 1 MB
+constexpr int GRAD_KEEP_CHUNKS = 2048;
+// Lists of at most GRAD_CLUSTER_CHUNKS chunks (1 MB) take the one-cluster kernel.
+// Through the binding the two launches of the other form take about 10.5 us of
+// host time, whatever they read; the cluster's one takes 7.1, and 4.6, 5.3, 6.2 us
+// on the device for the norm of 256 KB, 512 KB, 1 MB (clipped 6.2, 6.2, 10.2) but
+// 8.2 (14.3) for 2 MB.  CTAs of 1024 threads: 6.2, 6.2, 6.2 (8.2, 10.3, 10.3).
+constexpr int GRAD_CLUSTER_CHUNKS = 32;
 constexpr int GRAD_CLUSTER_THREADS = 512;
 constexpr int GRAD_CLUSTER_MAX = 8;                            // CTAs
+static_assert(GRAD_CLUSTER_CHUNKS <= GRAD_SHORT_TENSORS, "a tensor has one chunk at least");
 
 enum GradNorm : int { GRAD_L1 = 1, GRAD_L2 = 2, GRAD_INF = 3 };
 

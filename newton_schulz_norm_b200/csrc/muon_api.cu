@@ -1125,7 +1125,7 @@ int run_grad_long(DeviceCtx* ctx, const GradList& a, const GradCall& call, cudaS
   L.h = call;
   L.h.npartials = 0;
   L.scales = a.outs != nullptr;
-  const int most = std::min(GRAD_MAX_CTAS, ctx->num_sms * std::min(GRAD_PARTIAL_CTAS, ctx->grad_blocks_per_sm));
+  const int most = std::min(GRAD_MAX_CTAS, ctx->num_sms * ctx->grad_blocks_per_sm);
   int rc = grad_walk(a, L, [&]() -> int {
     const int grid = std::min(L.nchunks, most);
     L.part0 = L.h.npartials;

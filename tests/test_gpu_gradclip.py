@@ -92,7 +92,7 @@ def _scale64(want, max_norm, eps):
     return min(1.0, max_norm / (want + eps)) if want + eps > 0 else 1.0
 
 
-SIZES = [1, 2, 3, 5, 7, 8, 9, 255, 1023, 1024, 1025, 4095, 4096, 4097, 8191, 8192, 8193, 16383, 16385, 100003]
+SIZES = [1, 2, 3, 5, 7, 8, 9, 255, 1023, 1024, 1025, 4097, 8191, 8192, 8193, 16383, 16384, 16385, 32769, 100003]
 
 
 # ---------------------------------------------------------------- the norm
@@ -646,10 +646,11 @@ def test_profiler_counts_the_launches(muon):
 
 
 def test_around_the_border_of_the_two_forms(muon):
-    """64 chunks of 16 KB: the longest list of one cluster, and one vector more;
-    64 and 65 small tensors."""
-    n = 64 * 4096
-    for sizes in ([n], [n + 1], [n - 1], [n - 4096, 4096], [n - 4096, 4097], [5] * 64, [5] * 65, [0] * 9 + [n]):
+    """32 chunks of 32 KB: the longest list of one cluster, and one element more;
+    32 and 33 small tensors, 64 and 65 (two sizes of table)."""
+    n = 32 * 8192
+    for sizes in ([n], [n + 1], [n - 1], [n - 8192, 8192], [n - 8192, 8193], [5] * 32, [5] * 33, [5] * 64, [5] * 65,
+                  [0] * 9 + [n]):
         gs, bases = _grads(sizes, [torch.float32], seed=80)
         outs, obases = _grads(sizes, [torch.bfloat16], seed=81, offs=[8])
         for p in (1.0, 2.0, INF):
