@@ -238,7 +238,8 @@ def capture_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor],
     step on the same tensors: write each step's gradients into ``grads`` in
     place before replaying.  The graph keeps the hyper-parameters it was
     captured with, but reads ``grad_scale`` (when given) anew each time: write
-    each step's scale into that tensor before replaying.  Launching nothing but kernels and one memset, a replay
+    each step's scale into that tensor before replaying, and keep it as long as
+    the graph, like every other tensor of the step.  Launching nothing but kernels and one memset, a replay
     saves the host work and launch gaps of the eager call.
     """
     kw = dict(lr=lr, beta=beta, nesterov=nesterov, ns_steps=ns_steps, coeffs=coeffs,
@@ -462,19 +463,19 @@ class GradGroup:
     def norm(self, norm_type: float = 2.0, stream=None) -> torch.Tensor:
         """The norm over every gradient of the group, as a 0-d fp32 tensor.
         ``norm_type``: 1, 2 or inf (the largest magnitude)."""
-        return self._call(self._args, norm_type, _INF, 0.0, False, stream)
+        return self._call(self._args, float(norm_type), _INF, 0.0, False, stream)
 
     def clip_scale(self, max_norm: float, norm_type: float = 2.0, eps: float = 1e-6, stream=None):
         """(norm, scale): the norm, and min(1, max_norm / (norm + eps)) to be
         passed to the steps as ``grad_scale``.  Both 0-d fp32 tensors."""
-        return self._call(self._args, norm_type, max_norm, eps, True, stream)
+        return self._call(self._args, float(norm_type), float(max_norm), float(eps), True, stream)
 
     def clip(self, max_norm: float, norm_type: float = 2.0, eps: float = 1e-6, stream=None) -> torch.Tensor:
         """Multiplies every gradient by min(1, max_norm / (norm + eps)), in
         place or into ``out``, and returns the norm they had."""
         if not self._clippable:
             raise ValueError("tensors that clip writes must not overlap other tensors of the group")
-        return self._call(self._clip_args, norm_type, max_norm, eps, False, stream)
+        return self._call(self._clip_args, float(norm_type), float(max_norm), float(eps), False, stream)
 
 
 def grad_norm(grads: Sequence[torch.Tensor], norm_type: float = 2.0, stream=None) -> torch.Tensor:

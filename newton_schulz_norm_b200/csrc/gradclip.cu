@@ -509,11 +509,17 @@ int grad_blocks_per_sm(bool scale) {
 cudaError_t launch_grad_partial(const GradLaunch<GRAD_SHORT_TENSORS>& L, int grid, cudaStream_t stream) {
   return launch_partial(L, grid, stream);
 }
+cudaError_t launch_grad_partial(const GradLaunch<GRAD_MIDDLE_TENSORS>& L, int grid, cudaStream_t stream) {
+  return launch_partial(L, grid, stream);
+}
 cudaError_t launch_grad_partial(const GradLaunch<GRAD_MAX_TENSORS>& L, int grid, cudaStream_t stream) {
   return launch_partial(L, grid, stream);
 }
 cudaError_t launch_grad_scale(const GradLaunch<GRAD_SHORT_TENSORS>& L, int grid, cudaStream_t stream) {
   return launch_with(grad_scale_kernel<GRAD_SHORT_TENSORS>, grid, GRAD_THREADS, stream, true, 0, L);
+}
+cudaError_t launch_grad_scale(const GradLaunch<GRAD_MIDDLE_TENSORS>& L, int grid, cudaStream_t stream) {
+  return launch_with(grad_scale_kernel<GRAD_MIDDLE_TENSORS>, grid, GRAD_THREADS, stream, true, 0, L);
 }
 cudaError_t launch_grad_scale(const GradLaunch<GRAD_MAX_TENSORS>& L, int grid, cudaStream_t stream) {
   return launch_with(grad_scale_kernel<GRAD_MAX_TENSORS>, grid, GRAD_THREADS, stream, true, 0, L);

@@ -1178,10 +1178,11 @@ int run_grad(const GradList& a, const GradCall& call, cudaStream_t stream) {
     L.in_place = 1;
     return go();
   }
-  for (int i = 0, k = 0; i < a.n; ++i)
-    if (a.numels[i] > 0 && ++k > GRAD_SHORT_TENSORS)
-      return run_grad_long<GRAD_MAX_TENSORS>(ctx, a, call, stream);
-  return run_grad_long<GRAD_SHORT_TENSORS>(ctx, a, call, stream);
+  held = 0;
+  for (int i = 0; i < a.n; ++i) held += a.numels[i] > 0;
+  if (held <= GRAD_SHORT_TENSORS) return run_grad_long<GRAD_SHORT_TENSORS>(ctx, a, call, stream);
+  if (held <= GRAD_MIDDLE_TENSORS) return run_grad_long<GRAD_MIDDLE_TENSORS>(ctx, a, call, stream);
+  return run_grad_long<GRAD_MAX_TENSORS>(ctx, a, call, stream);
 }
 
 }  // namespace
@@ -1197,10 +1198,10 @@ using namespace muon;
 
 extern "C" {
 
-int muon_step_scaled(float* const* params, const float* const* grads, float* const* bufs,
-                     const int64_t* shapes, int n, float lr, float beta, int nesterov, int ns_steps,
-                     const float* coeffs, float* const* mirrors, int n_mirrors,
-                     const float* grad_scale, void* stream) {
+static int step_scaled_checked(float* const* params, const float* const* grads, float* const* bufs,
+                               const int64_t* shapes, int n, float lr, float beta, int nesterov,
+                               int ns_steps, const float* coeffs, float* const* mirrors, int n_mirrors,
+                               const float* grad_scale, void* stream) {
   int rc = check_shapes(shapes, n);
   if (rc) return rc;
   if (!scale_ok(grad_scale)) return MUON_ERR_UNSUPPORTED;
@@ -1246,6 +1247,16 @@ int muon_step_scaled(float* const* params, const float* const* grads, float* con
   return MUON_OK;
 }
 
+int muon_step_scaled(float* const* params, const float* const* grads, float* const* bufs,
+                     const int64_t* shapes, int n, float lr, float beta, int nesterov, int ns_steps,
+                     const float* coeffs, float* const* mirrors, int n_mirrors, const float* grad_scale,
+                     void* stream) {
+  return guarded([&] {
+    return step_scaled_checked(params, grads, bufs, shapes, n, lr, beta, nesterov, ns_steps, coeffs,
+                               mirrors, n_mirrors, grad_scale, stream);
+  });
+}
+
 int muon_step_mirrored(float* const* params, const float* const* grads, float* const* bufs,
                        const int64_t* shapes, int n, float lr, float beta, int nesterov,
                        int ns_steps, const float* coeffs, float* const* mirrors, int n_mirrors,
@@ -1261,11 +1272,11 @@ int muon_step(float* const* params, const float* const* grads, float* const* buf
                           nullptr, stream);
 }
 
-int muon_adamw_step_scaled(float* const* params, const float* const* grads, float* const* exp_avgs,
-                           float* const* exp_avg_sqs, const int64_t* numels,
-                           const unsigned char* decay, int n, int64_t step, double lr, double beta1,
-                           double beta2, double eps, double weight_decay, const float* grad_scale,
-                           void* stream) {
+static int adamw_step_scaled_checked(float* const* params, const float* const* grads,
+                                     float* const* exp_avgs, float* const* exp_avg_sqs,
+                                     const int64_t* numels, const unsigned char* decay, int n,
+                                     int64_t step, double lr, double beta1, double beta2, double eps,
+                                     double weight_decay, const float* grad_scale, void* stream) {
   if (n < 0) return MUON_ERR_INVALID_ARG;
   if (!scale_ok(grad_scale)) return MUON_ERR_UNSUPPORTED;
   if (n == 0) return MUON_OK;
@@ -1344,6 +1355,16 @@ int muon_adamw_step_scaled(float* const* params, const float* const* grads, floa
   return flush();
 }
 
+int muon_adamw_step_scaled(float* const* params, const float* const* grads, float* const* exp_avgs,
+                           float* const* exp_avg_sqs, const int64_t* numels, const unsigned char* decay,
+                           int n, int64_t step, double lr, double beta1, double beta2, double eps,
+                           double weight_decay, const float* grad_scale, void* stream) {
+  return guarded([&] {
+    return adamw_step_scaled_checked(params, grads, exp_avgs, exp_avg_sqs, numels, decay, n, step, lr,
+                                     beta1, beta2, eps, weight_decay, grad_scale, stream);
+  });
+}
+
 int muon_adamw_step(float* const* params, const float* const* grads, float* const* exp_avgs,
                     float* const* exp_avg_sqs, const int64_t* numels, const unsigned char* decay,
                     int n, int64_t step, double lr, double beta1, double beta2, double eps,
@@ -1379,6 +1400,8 @@ int muon_clip_grads(const void* const* grads, const unsigned char* dtypes, const
   if (outs) {
     rc = check_grad_list(outs, out_dtypes, numels, n);
     if (rc) return rc;
+    for (int i = 0; i < n; ++i)
+      if (numels[i] > 0 && outs[i] == grads[i] && out_dtypes[i] != dtypes[i]) return MUON_ERR_INVALID_ARG;
   }
   if ((reinterpret_cast<uintptr_t>(norm) & 3u) || !scale_ok(scale) ||
       (reinterpret_cast<uintptr_t>(workspace) & 7u))
@@ -1440,9 +1463,10 @@ int muon_momentum_normalize(const float* const* grads, float* const* bufs, uint1
   return muon_momentum_normalize_scaled(grads, bufs, x0, x0_ld, shapes, n, beta, nesterov, nullptr, stream);
 }
 
-int muon_momentum_normalize_scaled(const float* const* grads, float* const* bufs, uint16_t* const* x0,
-                                   const int64_t* x0_ld, const int64_t* shapes, int n, float beta,
-                                   int nesterov, const float* grad_scale, void* stream) {
+static int momentum_normalize_scaled_checked(const float* const* grads, float* const* bufs,
+                                             uint16_t* const* x0, const int64_t* x0_ld,
+                                             const int64_t* shapes, int n, float beta, int nesterov,
+                                             const float* grad_scale, void* stream) {
   int rc = check_shapes(shapes, n);
   if (rc) return rc;
   if (!scale_ok(grad_scale)) return MUON_ERR_UNSUPPORTED;
@@ -1476,6 +1500,15 @@ int muon_momentum_normalize_scaled(const float* const* grads, float* const* bufs
   }
   return run_k1(ctx, P, ptrs.data(), K1_MOMENTUM, beta, nesterov, grad_scale,
                 static_cast<cudaStream_t>(stream));
+}
+
+int muon_momentum_normalize_scaled(const float* const* grads, float* const* bufs, uint16_t* const* x0,
+                                   const int64_t* x0_ld, const int64_t* shapes, int n, float beta,
+                                   int nesterov, const float* grad_scale, void* stream) {
+  return guarded([&] {
+    return momentum_normalize_scaled_checked(grads, bufs, x0, x0_ld, shapes, n, beta, nesterov,
+                                             grad_scale, stream);
+  });
 }
 
 // One GEMM phase on caller buffers (stage entry points).

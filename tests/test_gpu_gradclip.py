@@ -280,6 +280,15 @@ def test_the_same_clip_again_and_again(muon):
         assert abs(float(norm) - 1.0) <= 1e-6 + 4 * U
 
 
+def test_numbers_of_other_kinds_as_arguments(muon):
+    g = [torch.full((500,), 2.0, device="cuda")]
+    a = muon.clip_scale(g, 1.0, 2.0)
+    for mx, p in ((np.float32(1.0), 2), (torch.tensor(1.0), np.float32(2.0)), (1, "2")):
+        b = muon.clip_scale(g, mx, p)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    assert float(muon.grad_norm(g, "inf")) == 2.0
+
+
 def test_values_are_read_anew_by_every_call(muon):
     g = torch.ones(1000, device="cuda")
     group = muon.GradGroup([g])
@@ -501,6 +510,23 @@ def test_nan_scale_spoils_the_step_and_no_gradient(muon):
     assert bool(torch.isnan(p).all()) and bool(torch.isnan(b).all()) and torch.equal(g, keep)
 
 
+def test_sharded_step_takes_the_scale(muon):
+    """One process: the owned matrices are all of them."""
+    from newton_schulz_norm_b200.sharded import ShardedMuon
+    rng = np.random.default_rng(68)
+    shapes = [(96, 64), (64, 200)]
+    p, g = ([rng.standard_normal(x).astype(np.float32) for x in shapes] for _ in range(2))
+    sm = ShardedMuon(shapes)
+    for v, x in zip(sm.params, p):
+        v.copy_(torch.from_numpy(x))
+    G, P, B = _dev(g), _dev(p), [torch.zeros(x, device="cuda") for x in shapes]
+    norm, scale = muon.clip_scale(G, 1.0)
+    sm.step(G, lr=0.02, grad_scale=scale)
+    muon.step(P, G, B, lr=0.02, grad_scale=scale)
+    for a, b in zip(list(sm.params) + [sm.bufs[0], sm.bufs[1]], P + B):
+        assert torch.equal(a, b)
+
+
 def test_captured_step_reads_the_scale_anew(muon):
     wl = WORKLOADS["gpt2_block"]
     st = WorkloadStream(wl, seed=66)
@@ -647,10 +673,10 @@ def test_profiler_counts_the_launches(muon):
 
 def test_around_the_border_of_the_two_forms(muon):
     """32 chunks of 32 KB: the longest list of one cluster, and one element more;
-    32 and 33 small tensors, 64 and 65 (two sizes of table)."""
+    32 and 33 small tensors, then the borders of the three sizes of table."""
     n = 32 * 8192
     for sizes in ([n], [n + 1], [n - 1], [n - 8192, 8192], [n - 8192, 8193], [5] * 32, [5] * 33, [5] * 64, [5] * 65,
-                  [0] * 9 + [n]):
+                  [5] * 256, [5] * 257, [5] * 512, [5] * 513, [0] * 9 + [n], [0] * 600 + [n, n]):
         gs, bases = _grads(sizes, [torch.float32], seed=80)
         outs, obases = _grads(sizes, [torch.bfloat16], seed=81, offs=[8])
         for p in (1.0, 2.0, INF):

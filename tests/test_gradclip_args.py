@@ -64,6 +64,7 @@ def test_refusals_of_results_and_outputs(muon):
     assert _clip(lib, outs=(P * 1)(P(None))) == -1
     assert _clip(lib, outs=(P * 1)(P(130))) == -2
     assert _clip(lib, out_types=(ctypes.c_ubyte * 1)(7)) == -1
+    assert _clip(lib, outs=(P * 1)(P(64)), out_types=(ctypes.c_ubyte * 1)(1)) == -1   # in place, another type
 
 
 def test_refusals_of_the_scaled_steps(muon):
@@ -133,3 +134,15 @@ def test_which_outputs_may_be_written(muon):
     big, inside = base[:40], base[4:6]
     assert not ok([inside, b], [big, c])
     assert not ok([base[60:], base[50:60], a], [big, base[50:60], a])     # a long one over a later one
+
+
+def test_sharded_step_passes_the_scale_on():
+    """ShardedMuon.step hands grad_scale to its step function, and only then."""
+    from newton_schulz_norm_b200.sharded import ShardedMuon
+    seen = []
+    sm = ShardedMuon([(4, 8), (8, 4)], device="cpu", step_fn=lambda p, g, b, **kw: seen.append(kw))
+    grads = [torch.zeros(4, 8), torch.zeros(8, 4)]
+    scale = torch.tensor(0.5)
+    sm.step(grads, lr=0.1, grad_scale=scale)
+    sm.step(grads, lr=0.1)
+    assert seen[0]["grad_scale"] is scale and "grad_scale" not in seen[1]
