@@ -11,6 +11,7 @@ raise.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 from typing import Sequence
@@ -90,7 +91,7 @@ def library() -> ctypes.CDLL:
         "muon_clip_grads": (i, [_P, _P, _P, i, _P, _P, d, d, d, _P, _P, _P, i64, _P]),
         "muon_step_scaled": (i, [_PP, _PP, _PP, _I64P, i, f, f, i, i, _FP, _PP, i, _P, _P]),
         "muon_adamw_step_scaled": (i, [_P, _P, _P, _P, _P, _P, i, i64, d, d, d, d, d, _P, _P]),
-        "muon_momentum_normalize_scaled": (i, [_PP, _PP, _PP, _I64P, _I64P, i, f, i, _P, _P]),
+        "muon_momentum_normalize_scaled": (i, [_P, _P, _P, _P, _P, i, f, i, _P, _P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -138,10 +139,11 @@ def _scale_ptr(grad_scale):
     the current device), or None."""
     if grad_scale is None:
         return None
-    if not isinstance(grad_scale, torch.Tensor) or not grad_scale.is_cuda \
-            or grad_scale.dtype != torch.float32 or grad_scale.numel() != 1:
+    if not isinstance(grad_scale, torch.Tensor) or grad_scale.get_device() < 0 \
+            or grad_scale.dtype is not torch.float32 or grad_scale.numel() != 1:
         raise ValueError("grad_scale: expected a float32 CUDA tensor of one element")
-    _check_device(grad_scale.device.index, "grad_scale")
+    if grad_scale.get_device() != torch.cuda.current_device():
+        _check_device(grad_scale.get_device(), "grad_scale")
     return grad_scale.data_ptr()
 
 
@@ -152,7 +154,7 @@ def _check_device(index: int, name: str):
 
 
 def _check_mat(t: torch.Tensor, name: str, dtype=torch.float32):
-    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+    if not isinstance(t, torch.Tensor) or t.ndim != 2:
         raise ValueError(f"{name}: expected a 2-D tensor")
     if not t.is_cuda or t.dtype != dtype or not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous {dtype} CUDA tensor")
@@ -522,7 +524,11 @@ def momentum_normalize(grads, bufs, beta=0.95, nesterov=True, stream=None, grad_
     """The fused first kernel alone; returns oriented bf16 X0 views (m x n).
     ``grad_scale`` as for step."""
     n = len(grads)
-    lds, shapes, outs = [], [], []
+    if len(bufs) != n:
+        raise ValueError("grads and bufs must have the same length")
+    # host arrays of 8-byte entries (quicker made than ctypes')
+    gs, bs, xs, lds, shapes = (array.array("q") for _ in range(5))
+    outs = []
     for g, b in zip(grads, bufs):
         _check_mat(g, "grad")
         _check_mat(b, "buf")
@@ -534,11 +540,14 @@ def momentum_normalize(grads, bufs, beta=0.95, nesterov=True, stream=None, grad_
         # rows of ld elements, as a view of their first nn
         x = torch.empty_strided((m, nn), (ld, 1), dtype=torch.bfloat16, device=g.device)
         outs.append(x)
+        gs.append(g.data_ptr())
+        bs.append(b.data_ptr())
+        xs.append(x.data_ptr())
         lds.append(ld)
-        shapes += (r, c)
+        shapes.append(r)
+        shapes.append(c)
     code = library().muon_momentum_normalize_scaled(
-        _ptr_array(grads), _ptr_array(bufs), _ptr_array(outs), (ctypes.c_int64 * n)(*lds),
-        (ctypes.c_int64 * len(shapes))(*shapes), n, float(beta), int(bool(nesterov)),
+        *(a.buffer_info()[0] for a in (gs, bs, xs, lds, shapes)), n, float(beta), int(bool(nesterov)),
         _scale_ptr(grad_scale), _stream_ptr(stream))
     _check(code, "muon_momentum_normalize")
     return outs

@@ -306,6 +306,8 @@ def test_refusals_on_the_gpu(muon):
                  lambda: muon.clip_grads([a], 1.0, out=[b[:8]]), lambda: muon.clip_grads([a, a], 1.0),
                  lambda: muon.clip_grads([a, b], 1.0, out=[b, a]), lambda: muon.clip_grads([a], 1.0, out=[a.view(torch.int32)]),
                  lambda: muon.adamw_step([a], [b], [a], [b], 1, 1e-3, grad_scale=torch.ones(2, device="cuda")),
+                 lambda: muon.momentum_normalize([a.view(4, 4)], []),
+                 lambda: muon.momentum_normalize([a.view(4, 4)], [b.view(2, 8)]),
                  lambda: muon.step([a.view(4, 4)], [b.view(4, 4)], [a.view(4, 4)], 0.1, grad_scale=0.5)):
         with pytest.raises(ValueError):
             call()
