@@ -310,7 +310,8 @@ MUON_API int muon_clip_grads(const void* const* grads, const unsigned char* dtyp
  * them and reading them back.  grad_scale = NULL is the plain call.  A NaN
  * scale makes every state and parameter of the call NaN: read N first where
  * such a step is to be skipped.  Other arguments as in the plain calls;
- * mirrors may be NULL with n_mirrors = 0.
+ * mirrors may be NULL with n_mirrors = 0.  The allocation-free first kernel
+ * has no scaled form.
  */
 MUON_API int muon_step_scaled(float* const* params, const float* const* grads, float* const* bufs,
                               const int64_t* shapes, int n, float lr, float beta, int nesterov,
@@ -356,7 +357,8 @@ MUON_API int64_t muon_workspace_bytes(const int64_t* shapes, int n);
  *   7 the chain launch: every Gram, polynomial and X-update phase of a step
  *     but the last update (kinds 1-3 are then used only by the stage entry
  *     points)
- *   8 gradient norm   9 gradient scaling (muon_clip_grads)
+ *   8 gradient norm   9 gradient scaling (muon_clip_grads; for a short list
+ *     its one launch, which computes the norm too)
  * ms and launches are host arrays of at least nkinds entries.  Returns the
  * number of kinds written, or a negative status.
  */

@@ -134,9 +134,24 @@ def _coeffs(coeffs):
     return (ctypes.c_float * 3)(*[float(c) for c in coeffs])
 
 
-def _scale_ptr(grad_scale):
+def _torch_stream(stream):
+    """A torch stream for a stream argument (a stream object or a handle)."""
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    ptr = _stream_ptr(stream)
+    return torch.cuda.ExternalStream(ptr) if ptr else torch.cuda.default_stream()
+
+
+def _is_side(stream) -> bool:
+    """Whether a stream argument names another stream than torch's current one."""
+    return stream is not None and _stream_ptr(stream) != _stream_ptr(None)
+
+
+def _scale_ptr(grad_scale, stream=None):
     """Device address of a gradient scale (a one-element fp32 CUDA tensor on
-    the current device), or None."""
+    the current device), or None.  Where ``stream`` is not torch's current one
+    the allocator is told, so that a scale dropped after the call is not handed
+    out again before the kernels there have read it."""
     if grad_scale is None:
         return None
     if not isinstance(grad_scale, torch.Tensor) or grad_scale.get_device() < 0 \
@@ -144,6 +159,8 @@ def _scale_ptr(grad_scale):
         raise ValueError("grad_scale: expected a float32 CUDA tensor of one element")
     if grad_scale.get_device() != torch.cuda.current_device():
         _check_device(grad_scale.get_device(), "grad_scale")
+    if _is_side(stream):
+        grad_scale.record_stream(_torch_stream(stream))
     return grad_scale.data_ptr()
 
 
@@ -153,11 +170,14 @@ def _check_device(index: int, name: str):
                          f"cuda:{torch.cuda.current_device()}")
 
 
-def _check_mat(t: torch.Tensor, name: str, dtype=torch.float32):
+def _check_mat(t: torch.Tensor, name: str, dtype=torch.float32, device: int | None = None):
+    """``device``: index of the current device, where the caller has it."""
     if not isinstance(t, torch.Tensor) or t.ndim != 2:
         raise ValueError(f"{name}: expected a 2-D tensor")
     if not t.is_cuda or t.dtype != dtype or not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous {dtype} CUDA tensor")
+    if t.get_device() != (torch.cuda.current_device() if device is None else device):
+        _check_device(t.get_device(), name)
 
 
 def _as_matrix(t: torch.Tensor) -> torch.Tensor:
@@ -197,9 +217,10 @@ def step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor],
         grads = [_as_matrix(t) for t in grads]
         bufs = [_as_matrix(t) for t in bufs]
     shapes = []
+    device = torch.cuda.current_device() if n else None
     for p, g, b in zip(params, grads, bufs):
         for t, nm in ((p, "param"), (g, "grad"), (b, "buf")):
-            _check_mat(t, nm)
+            _check_mat(t, nm, device=device)
         if g.shape != p.shape or b.shape != p.shape:
             raise ValueError("param, grad and buf shapes differ")
         shapes += [p.shape[0], p.shape[1]]
@@ -222,7 +243,7 @@ def step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor],
     code = library().muon_step_scaled(
         _ptr_array(params), _ptr_array(grads), _ptr_array(bufs), sh, n, float(lr), float(beta),
         int(bool(nesterov)), int(ns_steps), _coeffs(coeffs), mir, len(mirrors),
-        _scale_ptr(grad_scale), _stream_ptr(stream))
+        _scale_ptr(grad_scale, stream), _stream_ptr(stream))
     _check(code, "muon_step_mirrored" if mirrors else "muon_step")
 
 
@@ -241,8 +262,9 @@ def capture_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor],
     place before replaying.  The graph keeps the hyper-parameters it was
     captured with, but reads ``grad_scale`` (when given) anew each time: write
     each step's scale into that tensor before replaying, and keep it as long as
-    the graph, like every other tensor of the step.  Launching nothing but kernels and one memset, a replay
-    saves the host work and launch gaps of the eager call.
+    the graph, like every other tensor of the step.  Launching nothing but
+    kernels and one memset, a replay saves the host work and launch gaps of the
+    eager call.
     """
     kw = dict(lr=lr, beta=beta, nesterov=nesterov, ns_steps=ns_steps, coeffs=coeffs,
               reshape_nd=reshape_nd, grad_scale=grad_scale)
@@ -284,18 +306,21 @@ def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor],
     if decay is not None and len(decay) != n:
         raise ValueError("decay must have one entry per tensor")
     numels = []
+    device = torch.cuda.current_device() if n else None
     for p, g, m, v in zip(params, grads, exp_avgs, exp_avg_sqs):
         for t, nm in ((p, "param"), (g, "grad"), (m, "exp_avg"), (v, "exp_avg_sq")):
             if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.float32 \
                     or not t.is_contiguous():
                 raise ValueError(f"{nm}: expected a contiguous float32 CUDA tensor")
+            if t.get_device() != device:
+                _check_device(t.get_device(), nm)
         if g.shape != p.shape or m.shape != p.shape or v.shape != p.shape:
             raise ValueError("param, grad and average shapes differ")
         numels.append(p.numel())
     code = adamw_step_raw([t.data_ptr() for t in params], [t.data_ptr() for t in grads],
                           [t.data_ptr() for t in exp_avgs], [t.data_ptr() for t in exp_avg_sqs],
                           numels, step, lr, betas, eps, weight_decay, decay, _stream_ptr(stream),
-                          _scale_ptr(grad_scale))
+                          _scale_ptr(grad_scale, stream))
     _check(code, "muon_adamw_step")
 
 
@@ -318,11 +343,14 @@ class AdamWGroup:
             raise ValueError("params, grads, exp_avgs and exp_avg_sqs must have the same length")
         if decay is not None and len(decay) != n:
             raise ValueError("decay must have one entry per tensor")
+        self._device = params[0].get_device() if n and isinstance(params[0], torch.Tensor) else None
         for p, g, m, v in zip(params, grads, exp_avgs, exp_avg_sqs):
             for t, nm in ((p, "param"), (g, "grad"), (m, "exp_avg"), (v, "exp_avg_sq")):
                 if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.float32 \
                         or not t.is_contiguous():
                     raise ValueError(f"{nm}: expected a contiguous float32 CUDA tensor")
+                if t.get_device() != self._device:
+                    raise ValueError("every tensor must be on one device")
             if g.shape != p.shape or m.shape != p.shape or v.shape != p.shape:
                 raise ValueError("param, grad and average shapes differ")
         self._keep = (list(params), list(grads), list(exp_avgs), list(exp_avg_sqs))
@@ -342,9 +370,11 @@ class AdamWGroup:
              grad_scale: torch.Tensor | None = None) -> None:
         """One AdamW step (t = ``step``, from 1) on the group's tensors;
         ``grad_scale`` as for adamw_step."""
+        if self._device is not None and torch.cuda.current_device() != self._device:
+            _check_device(self._device, "params")
         code = library().muon_adamw_step_scaled(
             *self._args, int(step), self.lr if lr is None else float(lr), float(self.betas[0]),
-            float(self.betas[1]), self.eps, self.weight_decay, _scale_ptr(grad_scale),
+            float(self.betas[1]), self.eps, self.weight_decay, _scale_ptr(grad_scale, stream),
             _stream_ptr(stream))
         _check(code, "muon_adamw_step")
 
@@ -445,19 +475,19 @@ class GradGroup:
     def _call(self, args, p, max_norm, eps, with_scale, stream):
         if torch.cuda.current_device() != self._device:
             _check_device(self._device, "grads")
-        current = _raw_stream(self._device)
-        if stream is not None and _stream_ptr(stream) != current:
-            if not isinstance(stream, torch.cuda.Stream):
-                ptr = _stream_ptr(stream)
-                stream = torch.cuda.ExternalStream(ptr) if ptr else torch.cuda.default_stream()
-            with torch.cuda.stream(stream):     # the allocations below belong to that stream
-                return self._call(args, p, max_norm, eps, with_scale, None)
+        if _is_side(stream):
+            reader = torch.cuda.current_stream()
+            with torch.cuda.stream(_torch_stream(stream)):   # the allocations below belong to that stream
+                got = self._call(args, p, max_norm, eps, with_scale, None)
+            for t in got if with_scale else (got,):
+                t.record_stream(reader)
+            return got
         norm = torch.empty_like(self._result)
         scale = torch.empty_like(self._result) if with_scale else None
         work = None if self._work is None else torch.empty_like(self._work)
         code = library().muon_clip_grads(
             *args, p, max_norm, eps, norm.data_ptr(), None if scale is None else scale.data_ptr(),
-            None if work is None else work.data_ptr(), self._bytes, current)
+            None if work is None else work.data_ptr(), self._bytes, _raw_stream(self._device))
         if code:
             raise MuonError(code, "muon_grad_norm" if args is self._args else "muon_clip_grads")
         return (norm, scale) if with_scale else norm
@@ -526,12 +556,21 @@ def momentum_normalize(grads, bufs, beta=0.95, nesterov=True, stream=None, grad_
     n = len(grads)
     if len(bufs) != n:
         raise ValueError("grads and bufs must have the same length")
+    if _is_side(stream):
+        _scale_ptr(grad_scale, stream)
+        reader = torch.cuda.current_stream()
+        with torch.cuda.stream(_torch_stream(stream)):   # the X0s belong to that stream
+            outs = momentum_normalize(grads, bufs, beta, nesterov, None, grad_scale)
+        for x in outs:
+            x.record_stream(reader)
+        return outs
+    device = torch.cuda.current_device() if n else None
     # host arrays of 8-byte entries (quicker made than ctypes')
     gs, bs, xs, lds, shapes = (array.array("q") for _ in range(5))
     outs = []
     for g, b in zip(grads, bufs):
-        _check_mat(g, "grad")
-        _check_mat(b, "buf")
+        _check_mat(g, "grad", device=device)
+        _check_mat(b, "buf", device=device)
         if b.shape != g.shape:
             raise ValueError("grad and buf shapes differ")
         r, c = g.shape

@@ -373,6 +373,49 @@ def test_two_graphs_of_one_group(muon):
     del A, B
 
 
+def test_scales_dropped_while_a_side_stream_still_reads_them(muon):
+    """Each round's scale is computed on the current stream, read by steps on a
+    side stream behind a long queue, and dropped at once; so are X0s."""
+    side = torch.cuda.Stream()
+    rng = np.random.default_rng(55)
+    shape = (512, 512)
+    G = [torch.from_numpy(rng.standard_normal(shape).astype(np.float32)).cuda()]
+    P, B = [torch.zeros(shape, device="cuda")], [torch.zeros(shape, device="cuda")]
+    X0 = [torch.zeros(shape, device="cuda")]
+    flat = [torch.zeros(512 * 512, device="cuda") for _ in range(3)]
+    adamw = muon.AdamWGroup([flat[0]], [G[0].view(-1)], [flat[1]], [flat[2]], lr=1e-3)
+    torch.cuda.synchronize()
+    busy = torch.empty(1 << 28, device="cuda")
+    bounds = [3.0 * (k + 1) for k in range(12)]
+    kept = []
+    with torch.cuda.stream(side):
+        for _ in range(6):
+            busy.fill_(1.0)
+    for k, bound in enumerate(bounds):
+        scale = muon.clip_scale(G, bound)[1]
+        side.wait_stream(torch.cuda.current_stream())
+        muon.step(P, G, B, lr=0.02, stream=side, grad_scale=scale)
+        adamw.step(k + 1, stream=side, grad_scale=scale)
+        kept.append(muon.momentum_normalize(G, X0, stream=side, grad_scale=scale)[0])
+        del scale
+        junk = [torch.full((), -1.0, device="cuda") for _ in range(8)]   # takes freed places
+        del junk
+    norms = [muon.grad_norm(G, stream=side) for _ in range(3)]
+    torch.cuda.current_stream().wait_stream(side)
+    got = [t.clone() for t in P + B + X0 + flat + kept]
+    assert all(torch.equal(n, norms[0]) for n in norms)
+    for t in P + B + X0 + flat:
+        t.zero_()
+    want_kept = []
+    for k, bound in enumerate(bounds):
+        scale = muon.clip_scale(G, bound)[1]
+        muon.step(P, G, B, lr=0.02, grad_scale=scale)
+        adamw.step(k + 1, grad_scale=scale)
+        want_kept.append(muon.momentum_normalize(G, X0, grad_scale=scale)[0])
+    for a, b in zip(got, P + B + X0 + flat + want_kept):
+        assert torch.equal(a, b)
+
+
 # ---------------------------------------------------------------- the scaled steps
 
 def _dev(xs):

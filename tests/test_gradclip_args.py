@@ -146,3 +146,30 @@ def test_sharded_step_passes_the_scale_on():
     sm.step(grads, lr=0.1, grad_scale=scale)
     sm.step(grads, lr=0.1)
     assert seen[0]["grad_scale"] is scale and "grad_scale" not in seen[1]
+
+
+def test_another_device_than_the_current_one_is_refused(muon, monkeypatch):
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    muon._check_device(0, "grads")
+    with pytest.raises(ValueError, match="cuda:1"):
+        muon._check_device(1, "grads")
+
+    class OnDevice1(torch.Tensor):
+        is_cuda = True
+
+        def get_device(self):
+            return 1
+
+    t = torch.zeros(4, 4).as_subclass(OnDevice1)
+    with pytest.raises(ValueError, match="cuda:1"):
+        muon._check_mat(t, "grad")
+    with pytest.raises(ValueError, match="cuda:1"):
+        muon.step([t], [t], [t], 0.1)
+    with pytest.raises(ValueError, match="cuda:1"):
+        muon.momentum_normalize([t], [t])
+    with pytest.raises(ValueError, match="cuda:1"):
+        muon.adamw_step([t], [t], [t], [t], 1, 1e-3)
+    with pytest.raises(ValueError, match="cuda:1"):
+        muon.AdamWGroup([t], [t], [t], [t], lr=1e-3).step(1)
+    with pytest.raises(ValueError, match="cuda:1"):
+        muon._scale_ptr(torch.zeros(()).as_subclass(OnDevice1))
