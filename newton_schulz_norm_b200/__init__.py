@@ -565,28 +565,30 @@ def momentum_normalize(grads, bufs, beta=0.95, nesterov=True, stream=None, grad_
             x.record_stream(reader)
         return outs
     device = torch.cuda.current_device() if n else None
-    # host arrays of 8-byte entries (quicker made than ctypes')
-    gs, bs, xs, lds, shapes = (array.array("q") for _ in range(5))
-    outs = []
+    # One pass with few Python calls a matrix: for many small matrices this loop
+    # takes longer than the kernel (array is quicker than ctypes here).
+    tensor, f32, bf16, empty = torch.Tensor, torch.float32, torch.bfloat16, torch.empty_strided
+    ptrs, lds, shapes, outs = [], [], [], []
     for g, b in zip(grads, bufs):
-        _check_mat(g, "grad", device=device)
-        _check_mat(b, "buf", device=device)
-        if b.shape != g.shape:
+        shape = g.shape if isinstance(g, tensor) else ()
+        if not (isinstance(b, tensor) and len(shape) == 2 and b.shape == shape and g.dtype is f32
+                and b.dtype is f32 and g.get_device() == device and b.get_device() == device
+                and g.is_contiguous() and b.is_contiguous()):
+            _check_mat(g, "grad", device=device)
+            _check_mat(b, "buf", device=device)
             raise ValueError("grad and buf shapes differ")
-        r, c = g.shape
+        r, c = shape
         m, nn = (r, c) if r <= c else (c, r)
-        ld = _ld8(nn)
+        ld = (nn + 7) // 8 * 8
         # rows of ld elements, as a view of their first nn
-        x = torch.empty_strided((m, nn), (ld, 1), dtype=torch.bfloat16, device=g.device)
+        x = empty((m, nn), (ld, 1), dtype=bf16, device=g.device)
         outs.append(x)
-        gs.append(g.data_ptr())
-        bs.append(b.data_ptr())
-        xs.append(x.data_ptr())
+        ptrs += (g.data_ptr(), b.data_ptr(), x.data_ptr())
         lds.append(ld)
-        shapes.append(r)
-        shapes.append(c)
+        shapes += shape
+    host = [array.array("q", v) for v in (ptrs[0::3], ptrs[1::3], ptrs[2::3], lds, shapes)]
     code = library().muon_momentum_normalize_scaled(
-        *(a.buffer_info()[0] for a in (gs, bs, xs, lds, shapes)), n, float(beta), int(bool(nesterov)),
+        *(a.buffer_info()[0] for a in host), n, float(beta), int(bool(nesterov)),
         _scale_ptr(grad_scale), _stream_ptr(stream))
     _check(code, "muon_momentum_normalize")
     return outs
