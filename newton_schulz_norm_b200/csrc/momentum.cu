@@ -26,13 +26,14 @@
 // MUON_ERR_TIMEOUT instead of hanging.
 //
 // A gradient scale (clipping) is one multiplication on the way in, in both
-// passes; 245 us with it and without on the 48 matrices of GPT-2 124M, of
+// passes; 243 us with it, 242 without on the 48 matrices of GPT-2 124M, of
 // which the 14 bytes an element cannot do without take 182 us at the copy
 // rate.  What u is made of (plain, momentum, Nesterov) and whether a tile is
 // whole are template arguments: with both decided per element the same
 // launch took 260 us, and the four matrices of one block 37.6 instead of
-// 31.7 us.  Ragged tiles load a group of elements before they use the first:
-// three matrices with odd sides (129 x 1001 and the like) 24 instead of 48 us.
+// 31.7 us.  Ragged tiles load a group of elements, neighbours in neighbouring
+// threads, before they use the first: three matrices with odd sides (129 x 1001
+// and the like) 18 instead of 48 us.
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -114,11 +115,24 @@ __device__ __forceinline__ float u_from(float g, float bnew, float beta) {
   return RULE == RULE_NESTEROV ? fmaf(beta, bnew, g) : bnew;
 }
 
-// The thread's four runs of four columns of one 64 x 64 tile (rows lrow + 16 k),
-// all loaded before any is used.  WHOLE: the tile lies inside the matrix and
-// its rows are 16-byte aligned (c a multiple of 4).  Otherwise the elements are
-// loaded one by one, those outside as zero, RAGGED_RUNS runs at a time: all
-// four at once would cost the whole tiles registers.
+// The thread's four columns of rows lrow + 16 k of a tile: lcol .. lcol + 3, a
+// whole vector where rows are 16-byte aligned (c a multiple of 4); else, since
+// elements are then loaded one by one, every 16th column, so that neighbouring
+// threads load neighbouring elements.  Column e is col + e * step.
+struct Cols {
+  int col, step;
+};
+
+__device__ __forceinline__ Cols tile_cols(long long c, int tid) {
+  const int k = tid & 15;
+  return (c & 3) == 0 ? Cols{4 * k, 1} : Cols{k, 16};
+}
+
+// The thread's 4 x 4 entries of one 64 x 64 tile, all loaded before any is used.
+// WHOLE: the tile lies inside the matrix and its rows are 16-byte aligned.
+// Otherwise the elements are loaded one by one, those outside as zero,
+// RAGGED_RUNS rows at a time: all four at once would cost the whole tiles
+// registers.
 struct Runs {
   float4 g[4], b[4];
 };
@@ -126,7 +140,7 @@ constexpr int RAGGED_RUNS = 2;
 
 template <int RULE, bool WHOLE>
 __device__ __forceinline__ void load_runs(const K1Ptrs& P, long long r, long long c, long long gr0,
-                                          long long gc, uint64_t pol, Runs& R) {
+                                          long long gc, int step, uint64_t pol, Runs& R) {
 #pragma unroll
   for (int k = 0; k < (WHOLE ? 4 : RAGGED_RUNS); ++k) {
     const long long gr = gr0 + 16 * k;
@@ -139,13 +153,13 @@ __device__ __forceinline__ void load_runs(const K1Ptrs& P, long long r, long lon
     } else {
       const bool row = gr < r, has_buf = RULE != RULE_PLAIN;
       if (row && gc < c) R.g[k].x = P.g[off];
-      if (row && gc + 1 < c) R.g[k].y = P.g[off + 1];
-      if (row && gc + 2 < c) R.g[k].z = P.g[off + 2];
-      if (row && gc + 3 < c) R.g[k].w = P.g[off + 3];
+      if (row && gc + step < c) R.g[k].y = P.g[off + step];
+      if (row && gc + 2 * step < c) R.g[k].z = P.g[off + 2 * step];
+      if (row && gc + 3 * step < c) R.g[k].w = P.g[off + 3 * step];
       if (row && has_buf && gc < c) R.b[k].x = __ldcg(P.buf + off);
-      if (row && has_buf && gc + 1 < c) R.b[k].y = __ldcg(P.buf + off + 1);
-      if (row && has_buf && gc + 2 < c) R.b[k].z = __ldcg(P.buf + off + 2);
-      if (row && has_buf && gc + 3 < c) R.b[k].w = __ldcg(P.buf + off + 3);
+      if (row && has_buf && gc + step < c) R.b[k].y = __ldcg(P.buf + off + step);
+      if (row && has_buf && gc + 2 * step < c) R.b[k].z = __ldcg(P.buf + off + 2 * step);
+      if (row && has_buf && gc + 3 * step < c) R.b[k].w = __ldcg(P.buf + off + 3 * step);
     }
   }
 }
@@ -159,15 +173,17 @@ __device__ __forceinline__ bool whole_tile(const K1Info& q, long long r0, long l
 // fp32 first, in ragged tiles too.
 template <int RULE, bool SCALED, bool WHOLE>
 __device__ __forceinline__ double pass1_tile(const K1Launch& L, const K1Ptrs& P, long long r,
-                                             long long c, long long r0, long long c0, int lrow,
-                                             int lcol, float s, uint64_t pol) {
-  const long long gc = c0 + lcol;
+                                             long long c, long long r0, long long c0, int tid,
+                                             float s, uint64_t pol) {
   constexpr int RUNS = WHOLE ? 4 : RAGGED_RUNS;
+  const Cols C = WHOLE ? Cols{4 * (tid & 15), 1} : tile_cols(c, tid);
+  const int lrow = tid >> 4;
+  const long long gc = c0 + C.col;
   double ss = 0.0;
 #pragma unroll 1
   for (int k0 = 0; k0 < 4; k0 += RUNS) {
     Runs R;
-    load_runs<RULE, WHOLE>(P, r, c, r0 + lrow + 16 * k0, gc, pol, R);
+    load_runs<RULE, WHOLE>(P, r, c, r0 + lrow + 16 * k0, gc, C.step, pol, R);
 #pragma unroll
     for (int k = 0; k < RUNS; ++k) {
       const long long gr = r0 + lrow + 16 * (k0 + k);
@@ -176,7 +192,7 @@ __device__ __forceinline__ double pass1_tile(const K1Launch& L, const K1Ptrs& P,
       float u[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) u[e] = momentum_u<RULE>(taken<SCALED>(gv[e], s), bv[e], L.beta);
-      if (WHOLE || ((c & 3) == 0 && gr < r && gc + 4 <= c)) {
+      if (WHOLE || (C.step == 1 && gr < r && gc + 4 <= c)) {
         float sq = 0.f;
 #pragma unroll
         for (int e = 0; e < 4; ++e) sq = fmaf(u[e], u[e], sq);
@@ -187,9 +203,9 @@ __device__ __forceinline__ double pass1_tile(const K1Launch& L, const K1Ptrs& P,
         const long long off = gr * c + gc;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          if (gc + e < c) {
+          if (gc + e * C.step < c) {
             ss += (double)u[e] * (double)u[e];
-            if (RULE != RULE_PLAIN) P.buf[off + e] = bv[e];
+            if (RULE != RULE_PLAIN) P.buf[off + e * C.step] = bv[e];
           }
         }
       }
@@ -203,46 +219,58 @@ __device__ __forceinline__ double pass1_tile(const K1Launch& L, const K1Ptrs& P,
 template <int RULE, bool SCALED, bool WHOLE>
 __device__ __forceinline__ void pass2_tile(const K1Launch& L, const K1Ptrs& P, const K1Info& info,
                                            long long r0, long long c0, double inv, int tid,
-                                           int lrow, int lcol, uint16_t (*s_tile)[K1_TILE + 2],
-                                           float s, uint64_t pol) {
+                                           uint16_t (*s_tile)[K1_TILE + 2], float s, uint64_t pol) {
   const long long r = info.r, c = info.c;
   const bool tr = info.transposed != 0;
   constexpr int RUNS = WHOLE ? 4 : RAGGED_RUNS;
+  const Cols C = WHOLE ? Cols{4 * (tid & 15), 1} : tile_cols(c, tid);
+  const int lrow = tid >> 4;
 #pragma unroll 1
   for (int k0 = 0; k0 < 4; k0 += RUNS) {
     Runs R;
-    load_runs<RULE, WHOLE>(P, r, c, r0 + lrow + 16 * k0, c0 + lcol, pol, R);
+    load_runs<RULE, WHOLE>(P, r, c, r0 + lrow + 16 * k0, c0 + C.col, C.step, pol, R);
 #pragma unroll
     for (int k = 0; k < RUNS; ++k) {
       const int row = lrow + 16 * (k0 + k);
-      const long long gr = r0 + row;
-      const long long gc = c0 + lcol;
-      uint16_t bits[4] = {0, 0, 0, 0};
-      if (gr < r && gc < c) {
-        const float gv[4] = {R.g[k].x, R.g[k].y, R.g[k].z, R.g[k].w};
-        const float bv[4] = {R.b[k].x, R.b[k].y, R.b[k].z, R.b[k].w};
+      const float gv[4] = {R.g[k].x, R.g[k].y, R.g[k].z, R.g[k].w};
+      const float bv[4] = {R.b[k].x, R.b[k].y, R.b[k].z, R.b[k].w};
+      uint16_t bits[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float u = u_from<RULE>(taken<SCALED>(gv[e], s), bv[e], L.beta);
-          bits[e] = __bfloat16_as_ushort(__double2bfloat16((double)u * inv));
-        }
-        if (!tr) {
-          __nv_bfloat16* dst = P.x0 + gr * info.ldx + gc;
-          if (gc + 4 <= c) {
-            uint2 w;
-            w.x = (uint32_t)bits[0] | ((uint32_t)bits[1] << 16);
-            w.y = (uint32_t)bits[2] | ((uint32_t)bits[3] << 16);
-            st_hint_u2(dst, w, pol);
-          } else {
-            for (int e = 0; e < 4 && gc + e < c; ++e) dst[e] = __ushort_as_bfloat16(bits[e]);
-          }
-        }
+      for (int e = 0; e < 4; ++e) {
+        const float u = u_from<RULE>(taken<SCALED>(gv[e], s), bv[e], L.beta);
+        bits[e] = __bfloat16_as_ushort(__double2bfloat16((double)u * inv));
       }
-      if (tr) {
+      if (WHOLE && !tr) {
+        uint2 w;
+        w.x = (uint32_t)bits[0] | ((uint32_t)bits[1] << 16);
+        w.y = (uint32_t)bits[2] | ((uint32_t)bits[3] << 16);
+        st_hint_u2(P.x0 + (r0 + row) * info.ldx + (c0 + C.col), w, pol);
+      } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s_tile[row][lcol + e] = bits[e];
+        for (int e = 0; e < 4; ++e) s_tile[row][C.col + e * C.step] = bits[e];
       }
     }
+  }
+  if (!WHOLE && !tr) {
+    // X0 row by row, four columns a thread (ldx is a multiple of 8).
+    __syncthreads();
+    const int col = 4 * (tid & 15);
+    const long long gc = c0 + col;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int row = lrow + 16 * k;
+      const long long gr = r0 + row;
+      if (gr >= r || gc >= c) continue;
+      __nv_bfloat16* dst = P.x0 + gr * info.ldx + gc;
+      const uint16_t* q = &s_tile[row][col];
+      if (gc + 4 <= c) {
+        st_hint_u2(dst, make_uint2((uint32_t)q[0] | ((uint32_t)q[1] << 16),
+                                   (uint32_t)q[2] | ((uint32_t)q[3] << 16)), pol);
+      } else {
+        for (int e = 0; e < 4 && gc + e < c; ++e) dst[e] = __ushort_as_bfloat16(q[e]);
+      }
+    }
+    __syncthreads();   // s_tile is rewritten by the next tile
   }
   if (tr) {
     __syncthreads();
@@ -282,8 +310,6 @@ __global__ void __launch_bounds__(K1_THREADS, 4) k1_kernel(const __grid_constant
   const float s = SCALED ? __ldg(L.grad_scale) : 1.f;
   const uint64_t pol_keep = policy_evict_last();
   const uint64_t pol_drop = policy_evict_first();
-  const int lrow = tid >> 4;         // 0..15
-  const int lcol = (tid & 15) * 4;   // 0..60
 
   for (;;) {
     if (tid == 0) s_item = atomicAdd(L.counter, 1);
@@ -319,8 +345,8 @@ __global__ void __launch_bounds__(K1_THREADS, 4) k1_kernel(const __grid_constant
         const long long r0 = (long long)(t / info.tiles_c) * K1_TILE;
         const long long c0 = (long long)(t % info.tiles_c) * K1_TILE;
         ss += whole_tile(info, r0, c0)
-                  ? pass1_tile<RULE, SCALED, true>(L, P, info.r, info.c, r0, c0, lrow, lcol, s, pol_keep)
-                  : pass1_tile<RULE, SCALED, false>(L, P, info.r, info.c, r0, c0, lrow, lcol, s, pol_keep);
+                  ? pass1_tile<RULE, SCALED, true>(L, P, info.r, info.c, r0, c0, tid, s, pol_keep)
+                  : pass1_tile<RULE, SCALED, false>(L, P, info.r, info.c, r0, c0, tid, s, pol_keep);
       }
       const double tot = block_sum(ss, s_red);
       if (tid == 0) {
@@ -368,9 +394,9 @@ __global__ void __launch_bounds__(K1_THREADS, 4) k1_kernel(const __grid_constant
       const long long r0 = (long long)(t / info.tiles_c) * K1_TILE;
       const long long c0 = (long long)(t % info.tiles_c) * K1_TILE;
       if (whole_tile(info, r0, c0))
-        pass2_tile<RULE, SCALED, true>(L, P, info, r0, c0, inv, tid, lrow, lcol, s_tile, s, pol_drop);
+        pass2_tile<RULE, SCALED, true>(L, P, info, r0, c0, inv, tid, s_tile, s, pol_drop);
       else
-        pass2_tile<RULE, SCALED, false>(L, P, info, r0, c0, inv, tid, lrow, lcol, s_tile, s, pol_drop);
+        pass2_tile<RULE, SCALED, false>(L, P, info, r0, c0, inv, tid, s_tile, s, pol_drop);
     }
   }
 }
