@@ -280,6 +280,31 @@ def test_the_same_clip_again_and_again(muon):
         assert abs(float(norm) - 1.0) <= 1e-6 + 4 * U
 
 
+@pytest.mark.parametrize("sizes", [[40_000, 3], [2_500_000, 77], [9_000_001] * 2 + [11] * 600],
+                         ids=["cluster", "two_launches", "several_tables"])
+def test_writes_before_and_after_are_kept_apart(muon, sizes):
+    """Gradients written just before a clip in place and read just after it,
+    over and over without a wait: the second launch of the clip begins before
+    the first has ended, and must see neither older nor newer values."""
+    src = [[torch.randn(n, device="cuda") * (k + 1) for n in sizes] for k in range(3)]
+    g = [torch.empty(n, device="cuda") for n in sizes]
+    want = []
+    for xs in src:
+        _, scale = muon.clip_scale(xs, 1.0)
+        want.append([x * scale for x in xs])
+    group = muon.GradGroup(g)
+    bad = torch.zeros((), device="cuda")
+    for i in range(60):
+        for d, x in zip(g, src[i % 3]):
+            d.copy_(x)
+        group.clip(1.0)
+        for d, w in zip(g[:4], want[i % 3]):
+            bad += (d != w).any()
+    assert float(bad) == 0.0
+    for d, w in zip(g, want[59 % 3]):
+        assert torch.equal(d, w)
+
+
 def test_numbers_of_other_kinds_as_arguments(muon):
     g = [torch.full((500,), 2.0, device="cuda")]
     a = muon.clip_scale(g, 1.0, 2.0)
