@@ -170,7 +170,9 @@ __device__ __forceinline__ bool whole_tile(const K1Info& q, long long r0, long l
 
 // Pass 1 on one 64 x 64 tile: momentum (buf written back) and this thread's
 // sum of squares of u.  A run of four whole aligned columns sums its squares in
-// fp32 first, in ragged tiles too.
+// fp32 first, in ragged tiles too; where that leaves fp32 (|u| above 9e18), they
+// are formed and added in fp64, as single elements' are.  (What underflows is
+// below 1e-19 an element, nothing beside the 1e-7 that the norm is added to.)
 template <int RULE, bool SCALED, bool WHOLE>
 __device__ __forceinline__ double pass1_tile(const K1Launch& L, const K1Ptrs& P, long long r,
                                              long long c, long long r0, long long c0, int tid,
@@ -196,7 +198,13 @@ __device__ __forceinline__ double pass1_tile(const K1Launch& L, const K1Ptrs& P,
         float sq = 0.f;
 #pragma unroll
         for (int e = 0; e < 4; ++e) sq = fmaf(u[e], u[e], sq);
-        ss += (double)sq;
+        double run = (double)sq;
+        if (isinf(sq)) {
+          run = 0.0;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) run = fma((double)u[e], (double)u[e], run);
+        }
+        ss += run;
         if (RULE != RULE_PLAIN)
           st_hint(P.buf + gr * c + gc, make_float4(bv[0], bv[1], bv[2], bv[3]), pol);
       } else if (gr < r) {
