@@ -31,9 +31,11 @@
 // rate.  What u is made of (plain, momentum, Nesterov) and whether a tile is
 // whole are template arguments: with both decided per element the same
 // launch took 260 us, and the four matrices of one block 37.6 instead of
-// 31.7 us.  Ragged tiles load a group of elements, neighbours in neighbouring
-// threads, before they use the first: three matrices with odd sides (129 x 1001
-// and the like) 18 instead of 48 us.
+// 31.7 us.  Edge tiles of aligned rows load the same vectors as whole tiles, left
+// out where they lie outside (200000 x 60: 55.6 us, as 200000 x 64, against 76 us
+// by single elements).  Rows that are not aligned load two rows of four elements,
+// neighbours in neighbouring threads, before they use the first: three matrices
+// with odd sides (129 x 1001 and the like) 16 instead of 49 us.
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -115,41 +117,50 @@ __device__ __forceinline__ float u_from(float g, float bnew, float beta) {
   return RULE == RULE_NESTEROV ? fmaf(beta, bnew, g) : bnew;
 }
 
-// The thread's four columns of rows lrow + 16 k of a tile: lcol .. lcol + 3, a
-// whole vector where rows are 16-byte aligned (c a multiple of 4); else, since
-// elements are then loaded one by one, every 16th column, so that neighbouring
-// threads load neighbouring elements.  Column e is col + e * step.
+// How a tile is loaded.  WHOLE: it lies inside the matrix and rows are 16-byte
+// aligned (c a multiple of 4), so that every group of four columns is one
+// vector.  ALIGNED: the same vectors, those outside the matrix left out (a group
+// is inside or outside as a whole).  LOOSE: rows are not aligned and elements
+// are loaded one by one.
+enum Tile : int { TILE_WHOLE, TILE_ALIGNED, TILE_LOOSE };
+
+// The thread's four columns of rows lrow + 16 k of a tile: in vectors lcol ..
+// lcol + 3, one by one every 16th, so that neighbouring threads load
+// neighbouring elements.  Column e is col + e * step.
 struct Cols {
   int col, step;
 };
 
-__device__ __forceinline__ Cols tile_cols(long long c, int tid) {
+template <int TILE>
+__device__ __forceinline__ Cols tile_cols(int tid) {
   const int k = tid & 15;
-  return (c & 3) == 0 ? Cols{4 * k, 1} : Cols{k, 16};
+  return TILE == TILE_LOOSE ? Cols{k, 16} : Cols{4 * k, 1};
 }
 
-// The thread's 4 x 4 entries of one 64 x 64 tile, all loaded before any is used.
-// WHOLE: the tile lies inside the matrix and its rows are 16-byte aligned.
-// Otherwise the elements are loaded one by one, those outside as zero,
-// RAGGED_RUNS rows at a time: all four at once would cost the whole tiles
-// registers.
+// The thread's entries of one 64 x 64 tile, RUNS rows at a time, all loaded
+// before any is used; those outside the matrix are zero.  Four rows of single
+// elements would cost the other tiles registers.
+template <int TILE>
+constexpr int RUNS = TILE == TILE_LOOSE ? 2 : 4;
+
 struct Runs {
   float4 g[4], b[4];
 };
-constexpr int RAGGED_RUNS = 2;
 
-template <int RULE, bool WHOLE>
+template <int RULE, int TILE>
 __device__ __forceinline__ void load_runs(const K1Ptrs& P, long long r, long long c, long long gr0,
                                           long long gc, int step, uint64_t pol, Runs& R) {
 #pragma unroll
-  for (int k = 0; k < (WHOLE ? 4 : RAGGED_RUNS); ++k) {
+  for (int k = 0; k < RUNS<TILE>; ++k) {
     const long long gr = gr0 + 16 * k;
     const long long off = gr * c + gc;
     R.g[k] = make_float4(0.f, 0.f, 0.f, 0.f);
     R.b[k] = R.g[k];
-    if (WHOLE) {
-      R.g[k] = ld_hint(P.g + off, pol);
-      if (RULE != RULE_PLAIN) R.b[k] = ld_hint(P.buf + off, pol);
+    if (TILE != TILE_LOOSE) {
+      if (TILE == TILE_WHOLE || (gr < r && gc < c)) {
+        R.g[k] = ld_hint(P.g + off, pol);
+        if (RULE != RULE_PLAIN) R.b[k] = ld_hint(P.buf + off, pol);
+      }
     } else {
       const bool row = gr < r, has_buf = RULE != RULE_PLAIN;
       if (row && gc < c) R.g[k].x = P.g[off];
@@ -164,37 +175,37 @@ __device__ __forceinline__ void load_runs(const K1Ptrs& P, long long r, long lon
   }
 }
 
-__device__ __forceinline__ bool whole_tile(const K1Info& q, long long r0, long long c0) {
-  return (q.c & 3) == 0 && r0 + K1_TILE <= q.r && c0 + K1_TILE <= q.c;
+__device__ __forceinline__ int tile_kind(const K1Info& q, long long r0, long long c0) {
+  if ((q.c & 3) != 0) return TILE_LOOSE;
+  return r0 + K1_TILE <= q.r && c0 + K1_TILE <= q.c ? TILE_WHOLE : TILE_ALIGNED;
 }
 
 // Pass 1 on one 64 x 64 tile: momentum (buf written back) and this thread's
-// sum of squares of u.  A run of four whole aligned columns sums its squares in
-// fp32 first, in ragged tiles too; where that leaves fp32 (|u| above 9e18), they
+// sum of squares of u.  A vector of four columns sums its squares in fp32
+// first; where that leaves fp32 (|u| above 9e18), they
 // are formed and added in fp64, as single elements' are.  (What underflows is
 // below 1e-19 an element, nothing beside the 1e-7 that the norm is added to.)
-template <int RULE, bool SCALED, bool WHOLE>
+template <int RULE, bool SCALED, int TILE>
 __device__ __forceinline__ double pass1_tile(const K1Launch& L, const K1Ptrs& P, long long r,
                                              long long c, long long r0, long long c0, int tid,
                                              float s, uint64_t pol) {
-  constexpr int RUNS = WHOLE ? 4 : RAGGED_RUNS;
-  const Cols C = WHOLE ? Cols{4 * (tid & 15), 1} : tile_cols(c, tid);
+  const Cols C = tile_cols<TILE>(tid);
   const int lrow = tid >> 4;
   const long long gc = c0 + C.col;
   double ss = 0.0;
 #pragma unroll 1
-  for (int k0 = 0; k0 < 4; k0 += RUNS) {
+  for (int k0 = 0; k0 < 4; k0 += RUNS<TILE>) {
     Runs R;
-    load_runs<RULE, WHOLE>(P, r, c, r0 + lrow + 16 * k0, gc, C.step, pol, R);
+    load_runs<RULE, TILE>(P, r, c, r0 + lrow + 16 * k0, gc, C.step, pol, R);
 #pragma unroll
-    for (int k = 0; k < RUNS; ++k) {
+    for (int k = 0; k < RUNS<TILE>; ++k) {
       const long long gr = r0 + lrow + 16 * (k0 + k);
       const float gv[4] = {R.g[k].x, R.g[k].y, R.g[k].z, R.g[k].w};
       float bv[4] = {R.b[k].x, R.b[k].y, R.b[k].z, R.b[k].w};
       float u[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) u[e] = momentum_u<RULE>(taken<SCALED>(gv[e], s), bv[e], L.beta);
-      if (WHOLE || (C.step == 1 && gr < r && gc + 4 <= c)) {
+      if (TILE == TILE_WHOLE || (TILE == TILE_ALIGNED && gr < r && gc < c)) {
         float sq = 0.f;
 #pragma unroll
         for (int e = 0; e < 4; ++e) sq = fmaf(u[e], u[e], sq);
@@ -207,7 +218,7 @@ __device__ __forceinline__ double pass1_tile(const K1Launch& L, const K1Ptrs& P,
         ss += run;
         if (RULE != RULE_PLAIN)
           st_hint(P.buf + gr * c + gc, make_float4(bv[0], bv[1], bv[2], bv[3]), pol);
-      } else if (gr < r) {
+      } else if (TILE == TILE_LOOSE && gr < r) {
         const long long off = gr * c + gc;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -224,21 +235,20 @@ __device__ __forceinline__ double pass1_tile(const K1Launch& L, const K1Ptrs& P,
 
 // Pass 2 on one 64 x 64 tile: recompute u from g and the new buf, scale by
 // 1/(norm + eps) in double, round once to bf16 and store oriented.
-template <int RULE, bool SCALED, bool WHOLE>
+template <int RULE, bool SCALED, int TILE>
 __device__ __forceinline__ void pass2_tile(const K1Launch& L, const K1Ptrs& P, const K1Info& info,
                                            long long r0, long long c0, double inv, int tid,
                                            uint16_t (*s_tile)[K1_TILE + 2], float s, uint64_t pol) {
   const long long r = info.r, c = info.c;
   const bool tr = info.transposed != 0;
-  constexpr int RUNS = WHOLE ? 4 : RAGGED_RUNS;
-  const Cols C = WHOLE ? Cols{4 * (tid & 15), 1} : tile_cols(c, tid);
+  const Cols C = tile_cols<TILE>(tid);
   const int lrow = tid >> 4;
 #pragma unroll 1
-  for (int k0 = 0; k0 < 4; k0 += RUNS) {
+  for (int k0 = 0; k0 < 4; k0 += RUNS<TILE>) {
     Runs R;
-    load_runs<RULE, WHOLE>(P, r, c, r0 + lrow + 16 * k0, c0 + C.col, C.step, pol, R);
+    load_runs<RULE, TILE>(P, r, c, r0 + lrow + 16 * k0, c0 + C.col, C.step, pol, R);
 #pragma unroll
-    for (int k = 0; k < RUNS; ++k) {
+    for (int k = 0; k < RUNS<TILE>; ++k) {
       const int row = lrow + 16 * (k0 + k);
       const float gv[4] = {R.g[k].x, R.g[k].y, R.g[k].z, R.g[k].w};
       const float bv[4] = {R.b[k].x, R.b[k].y, R.b[k].z, R.b[k].w};
@@ -248,18 +258,19 @@ __device__ __forceinline__ void pass2_tile(const K1Launch& L, const K1Ptrs& P, c
         const float u = u_from<RULE>(taken<SCALED>(gv[e], s), bv[e], L.beta);
         bits[e] = __bfloat16_as_ushort(__double2bfloat16((double)u * inv));
       }
-      if (WHOLE && !tr) {
+      if (TILE != TILE_LOOSE && !tr) {
         uint2 w;
         w.x = (uint32_t)bits[0] | ((uint32_t)bits[1] << 16);
         w.y = (uint32_t)bits[2] | ((uint32_t)bits[3] << 16);
-        st_hint_u2(P.x0 + (r0 + row) * info.ldx + (c0 + C.col), w, pol);
+        if (TILE == TILE_WHOLE || (r0 + row < r && c0 + C.col < c))
+          st_hint_u2(P.x0 + (r0 + row) * info.ldx + (c0 + C.col), w, pol);
       } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e) s_tile[row][C.col + e * C.step] = bits[e];
       }
     }
   }
-  if (!WHOLE && !tr) {
+  if (TILE == TILE_LOOSE && !tr) {
     // X0 row by row, four columns a thread (ldx is a multiple of 8).
     __syncthreads();
     const int col = 4 * (tid & 15);
@@ -352,9 +363,13 @@ __global__ void __launch_bounds__(K1_THREADS, 4) k1_kernel(const __grid_constant
       for (int t = t0; t < t1; ++t) {
         const long long r0 = (long long)(t / info.tiles_c) * K1_TILE;
         const long long c0 = (long long)(t % info.tiles_c) * K1_TILE;
-        ss += whole_tile(info, r0, c0)
-                  ? pass1_tile<RULE, SCALED, true>(L, P, info.r, info.c, r0, c0, tid, s, pol_keep)
-                  : pass1_tile<RULE, SCALED, false>(L, P, info.r, info.c, r0, c0, tid, s, pol_keep);
+        const int kind = tile_kind(info, r0, c0);
+        if (kind == TILE_WHOLE)
+          ss += pass1_tile<RULE, SCALED, TILE_WHOLE>(L, P, info.r, info.c, r0, c0, tid, s, pol_keep);
+        else if (kind == TILE_ALIGNED)
+          ss += pass1_tile<RULE, SCALED, TILE_ALIGNED>(L, P, info.r, info.c, r0, c0, tid, s, pol_keep);
+        else
+          ss += pass1_tile<RULE, SCALED, TILE_LOOSE>(L, P, info.r, info.c, r0, c0, tid, s, pol_keep);
       }
       const double tot = block_sum(ss, s_red);
       if (tid == 0) {
@@ -401,10 +416,13 @@ __global__ void __launch_bounds__(K1_THREADS, 4) k1_kernel(const __grid_constant
     for (int t = t0; t < t1; ++t) {
       const long long r0 = (long long)(t / info.tiles_c) * K1_TILE;
       const long long c0 = (long long)(t % info.tiles_c) * K1_TILE;
-      if (whole_tile(info, r0, c0))
-        pass2_tile<RULE, SCALED, true>(L, P, info, r0, c0, inv, tid, s_tile, s, pol_drop);
+      const int kind = tile_kind(info, r0, c0);
+      if (kind == TILE_WHOLE)
+        pass2_tile<RULE, SCALED, TILE_WHOLE>(L, P, info, r0, c0, inv, tid, s_tile, s, pol_drop);
+      else if (kind == TILE_ALIGNED)
+        pass2_tile<RULE, SCALED, TILE_ALIGNED>(L, P, info, r0, c0, inv, tid, s_tile, s, pol_drop);
       else
-        pass2_tile<RULE, SCALED, false>(L, P, info, r0, c0, inv, tid, s_tile, s, pol_drop);
+        pass2_tile<RULE, SCALED, TILE_LOOSE>(L, P, info, r0, c0, inv, tid, s_tile, s, pol_drop);
     }
   }
 }
