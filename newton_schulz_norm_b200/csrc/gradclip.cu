@@ -148,6 +148,8 @@ __device__ __forceinline__ Acc<P> block_join(Acc<P> a, unsigned long long* red) 
 // walked in the aligned vectors that cover it: vector v holds elements
 // [v E - mis, (v + 1) E - mis).  Only the first and the last can be partial;
 // those are read element by element, so nothing outside the tensor is touched.
+// Gradients are read with coherent loads only: in place, the scaling writes what
+// the norm has read, in the same launch where one cluster does both.
 
 // Whether chunk v0.. of the tensor is nothing but whole vectors.
 __device__ __forceinline__ bool whole_chunk(const GradTensor& T, long long v0) {
@@ -164,7 +166,6 @@ struct Raw {
   uint4 v[GRAD_VEC];
 };
 
-// (Coherent loads: in place, the scaling writes what it reads here.)
 template <bool STREAMED>
 __device__ __forceinline__ void load_chunk(const GradTensor& T, long long v0, int tid, Raw& r) {
   const uint4* p = reinterpret_cast<const uint4*>(vector0(T)) + v0 + tid;
@@ -202,7 +203,7 @@ __device__ __forceinline__ void add_ragged(const GradTensor& T, long long v0, in
   for (long long v = v0 + tid; v < v1; v += GRAD_THREADS) {
     const long long e = v * E;
     if (e >= T.mis && e + E <= end) {
-      add_vec<P, DT>(__ldg(reinterpret_cast<const uint4*>(g) + v), acc);
+      add_vec<P, DT>(*(reinterpret_cast<const uint4*>(g) + v), acc);
     } else {
       for (int k = 0; k < E; ++k)
         if (e + k >= T.mis && e + k < end) acc.add(X::widen(g[e + k]));
