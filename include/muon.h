@@ -262,7 +262,7 @@ MUON_API int muon_adamw_step(float* const* params, const float* const* grads,
  *           numels[i] its element count (0 skips it; at most 2^40).
  *           Pointers need only be aligned to their element.
  *   p       1, 2 or INFINITY.
- *   max_norm  >= 0; INFINITY gives s = 1.      eps  >= 0, finite.
+ *   max_norm  >= 0; INFINITY gives s = 1 for every N but NaN.   eps  >= 0, finite.
  *   norm    device float (4-byte aligned): N, rounded once to fp32.
  *   scale   device float or NULL: s, formed in fp64 and rounded once.
  *   workspace  device memory, 8-byte aligned, of at least
@@ -276,7 +276,8 @@ MUON_API int muon_adamw_step(float* const* params, const float* const* grads,
  * overflows for finite fp32 input unless N itself does, and the same call on
  * the same device gives the same bits.  NaN and infinity go as the formulas
  * say: an infinite N gives s = 0 (and so NaN in the entries that were
- * infinite), a NaN N gives s = NaN.  N + eps = 0 gives s = 1.  With n = 0, or
+ * infinite) unless max_norm is infinite too, a NaN N gives s = NaN with every
+ * max_norm.  N + eps = 0 gives s = 1.  With n = 0, or
  * only empty tensors, N is 0 and is still written.
  */
 typedef enum { MUON_F32 = 0, MUON_BF16 = 1, MUON_F16 = 2 } muon_dtype_t;

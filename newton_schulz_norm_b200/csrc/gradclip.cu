@@ -258,8 +258,11 @@ __global__ void __launch_bounds__(GRAD_THREADS)
   if (threadIdx.x == 0) L.h.partials[L.part0 + blockIdx.x] = acc.word();
 }
 
-// s from N, in fp64 and from the unrounded N; a NaN norm gives a NaN scale.
+// s from N, in fp64 and from the unrounded N.  A NaN norm gives a NaN scale
+// whatever the bound; an infinite bound is never exceeded, not by an infinite
+// norm either (s = 1), which a finite one turns into s = 0.
 __device__ __forceinline__ float scale_of(double norm, const GradCall& h) {
+  if (isnan(norm)) return (float)norm;
   const double den = norm + h.eps;
   const double s = (isinf(h.max_norm) || den == 0.0) ? 1.0 : h.max_norm / den;
   return s >= 1.0 ? 1.f : (float)s;
