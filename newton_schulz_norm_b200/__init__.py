@@ -170,6 +170,13 @@ def _check_device(index: int, name: str):
                          f"cuda:{torch.cuda.current_device()}")
 
 
+def _device_for(tensors):
+    """Index of the current device, asked once for a list; None where the first
+    of the list is no CUDA tensor, which the checks of the list then refuse."""
+    t = next(iter(tensors), None)
+    return torch.cuda.current_device() if isinstance(t, torch.Tensor) and t.is_cuda else None
+
+
 def _check_mat(t: torch.Tensor, name: str, dtype=torch.float32, device: int | None = None):
     """``device``: index of the current device, where the caller has it."""
     if not isinstance(t, torch.Tensor) or t.ndim != 2:
@@ -217,7 +224,7 @@ def step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor],
         grads = [_as_matrix(t) for t in grads]
         bufs = [_as_matrix(t) for t in bufs]
     shapes = []
-    device = torch.cuda.current_device() if n else None
+    device = _device_for(params)
     for p, g, b in zip(params, grads, bufs):
         for t, nm in ((p, "param"), (g, "grad"), (b, "buf")):
             _check_mat(t, nm, device=device)
@@ -306,7 +313,7 @@ def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor],
     if decay is not None and len(decay) != n:
         raise ValueError("decay must have one entry per tensor")
     numels = []
-    device = torch.cuda.current_device() if n else None
+    device = _device_for(params)
     for p, g, m, v in zip(params, grads, exp_avgs, exp_avg_sqs):
         for t, nm in ((p, "param"), (g, "grad"), (m, "exp_avg"), (v, "exp_avg_sq")):
             if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.float32 \
@@ -564,7 +571,7 @@ def momentum_normalize(grads, bufs, beta=0.95, nesterov=True, stream=None, grad_
         for x in outs:
             x.record_stream(reader)
         return outs
-    device = torch.cuda.current_device() if n else None
+    device = _device_for(grads)
     # One pass with few Python calls a matrix: for many small matrices this loop
     # takes longer than the kernel (array is quicker than ctypes here).
     tensor, f32, bf16, empty = torch.Tensor, torch.float32, torch.bfloat16, torch.empty_strided

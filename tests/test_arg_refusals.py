@@ -1,0 +1,36 @@
+"""What the binding refuses before it asks for a GPU (none is needed here)."""
+import pytest
+import torch
+
+
+@pytest.fixture(scope="module")
+def muon():
+    from newton_schulz_norm_b200 import build
+    build.build()
+    import newton_schulz_norm_b200 as m
+    m.library()
+    return m
+
+
+def _calls(muon, t):
+    return {
+        "step": lambda: muon.step([t], [t], [t], 0.1),
+        "step nd": lambda: muon.step([t], [t], [t], 0.1, reshape_nd=True),
+        "capture_step": lambda: muon.capture_step([t], [t], [t], 0.1),
+        "adamw_step": lambda: muon.adamw_step([t], [t], [t], [t], 1, 1e-3),
+        "AdamWGroup": lambda: muon.AdamWGroup([t], [t], [t], [t], lr=1e-3),
+        "momentum_normalize": lambda: muon.momentum_normalize([t], [t]),
+        "orthogonalize": lambda: muon.orthogonalize(t),
+        "GradGroup": lambda: muon.GradGroup([t]),
+    }
+
+
+@pytest.mark.parametrize("call", list(_calls(None, None)))
+def test_tensors_off_the_gpu_are_a_value_error(muon, call):
+    """With a GPU and without one."""
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        _calls(muon, torch.zeros(4, 4))[call]()
+    for other in ("no tensor", None):
+        if call != "step nd":      # that one asks for the rank first
+            with pytest.raises(ValueError):
+                _calls(muon, other)[call]()
