@@ -350,7 +350,8 @@ class AdamWGroup:
             raise ValueError("params, grads, exp_avgs and exp_avg_sqs must have the same length")
         if decay is not None and len(decay) != n:
             raise ValueError("decay must have one entry per tensor")
-        self._device = params[0].get_device() if n and isinstance(params[0], torch.Tensor) else None
+        first = next(iter(params), None)
+        self._device = first.get_device() if isinstance(first, torch.Tensor) else None
         for p, g, m, v in zip(params, grads, exp_avgs, exp_avg_sqs):
             for t, nm in ((p, "param"), (g, "grad"), (m, "exp_avg"), (v, "exp_avg_sq")):
                 if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.float32 \

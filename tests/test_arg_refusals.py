@@ -34,3 +34,25 @@ def test_tensors_off_the_gpu_are_a_value_error(muon, call):
         if call != "step nd":      # that one asks for the rank first
             with pytest.raises(ValueError):
                 _calls(muon, other)[call]()
+
+
+def test_views_of_dicts_are_lists_too(muon, monkeypatch):
+    """Whatever has a length and can be walked again (a dict's values)."""
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+
+    class OnDevice0(torch.Tensor):
+        is_cuda = True
+
+        def get_device(self):
+            return 0
+
+    named = {k: torch.zeros(4, 4).as_subclass(OnDevice0) for k in "ab"}
+    values = named.values()
+    group = muon.AdamWGroup(values, values, values, values, lr=1e-3)
+    assert group._n == 2 and [group._p[i] for i in range(2)] == [t.data_ptr() for t in values]
+    off = {"a": torch.zeros(4, 4)}.values()
+    for call in (lambda: muon.AdamWGroup(off, off, off, off, lr=1e-3), lambda: muon.step(off, off, off, 0.1),
+                 lambda: muon.adamw_step(off, off, off, off, 1, 1e-3),
+                 lambda: muon.momentum_normalize(off, off), lambda: muon.GradGroup(off)):
+        with pytest.raises(ValueError, match="CUDA tensor"):
+            call()
