@@ -1134,7 +1134,7 @@ int run_grad_long(DeviceCtx* ctx, const GradList& a, const GradCall& call, cudaS
     return cuda_err(launch_grad_partial(L, grid, stream));
   });
   if (rc) return rc;
-  if (!a.outs || L.h.npartials == 0) {
+  if (!a.outs) {
     ProfScope ps(PK_GRAD_NORM, stream);
     return cuda_err(launch_grad_finish(L.h, stream));
   }
