@@ -4,11 +4,13 @@
  * newton_schulz_norm_b200.build with checked=True).  The regular libmuon.so
  * does not export them.
  *
- * In the checked build every kernel validates the entries of the tables it
- * reads (tile lists, problem tables, work items) against the sizes it was
- * launched with before using them, and turns an invalid entry into
- * MUON_ERR_INVALID_ARG in the status word (reported by muon_status) instead
- * of an access out of bounds.  The entry point below lets a test plant such
+ * In the checked build the GEMM kernels and the first kernel validate the
+ * entries of the tables that they read from device memory (tile lists, problem
+ * tables, work items) against the sizes they were launched with before using
+ * them, and turn an invalid entry into MUON_ERR_INVALID_ARG in the status word
+ * (reported by muon_status) instead of an access out of bounds.  The tables of
+ * the AdamW and gradient kernels are kernel arguments, filled by each call from
+ * arguments it has checked.  The entry point below lets a test plant such
  * an entry.  There is no counterpart of either on the pages; they are this
  * library's stand-in for a memory checker.
  */

@@ -429,6 +429,9 @@ class GradGroup:
     gradients into the fp32 ones that the steps take, for instance); an entry
     may be the gradient itself, none may overlap anything else.
 
+    Nothing is recorded for autograd: norms and scales are detached, whatever
+    the tensors require.
+
     Every call takes its workspace and its results from torch's allocator on
     the call's stream, so calls on several streams and captures in several
     graphs do not disturb one another.  The library's first call on a device

@@ -20,9 +20,10 @@ ROOT = os.path.dirname(PKG_DIR)
 CSRC = os.path.join(PKG_DIR, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_PATH = os.path.join(PKG_DIR, "libmuon.so")
-# The same sources with -DMUON_BOUNDS_CHECK: every kernel validates its table
-# entries and reports MUON_ERR_INVALID_ARG instead of reading out of bounds
-# (include/muon_debug.h).  For tests; the product path loads LIB_PATH.
+# The same sources with -DMUON_BOUNDS_CHECK: the GEMM kernels and the first
+# kernel validate the entries of their tables in device memory and report
+# MUON_ERR_INVALID_ARG instead of reading out of bounds (include/muon_debug.h).
+# For tests; the product path loads LIB_PATH.
 CHECKED_LIB_PATH = os.path.join(PKG_DIR, "libmuon_checked.so")
 
 ARCH_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a"]

@@ -236,7 +236,9 @@ __device__ __forceinline__ int add_chunks_to(const GradLaunch<N>& L, int c, int 
 
 // The norm's part of chunks first, first + step, ... of the launch.  Where the
 // gradients are scaled afterwards, the chunks that the scaling reads first (the
-// last ones) are left in L2 by passing the ones before through as streamed.
+// last ones) are left in L2 by passing the ones before through as streamed.  That
+// is so for a list of one launch; the scaling of a longer one begins with the
+// first launch's chunks, of which little is left by then.
 template <int P, int N>
 __device__ __forceinline__ Acc<P> add_chunks(const GradLaunch<N>& L, int first, int step, int tid) {
   Acc<P> acc;

@@ -11,11 +11,14 @@
 namespace muon {
 
 // Built with -DMUON_BOUNDS_CHECK (newton_schulz_norm_b200.build, checked=True),
-// every kernel validates the indices it reads from its tables (tile lists,
-// problem and work-item tables) against the sizes it was launched with before
-// using them; an invalid entry records MUON_ERR_INVALID_ARG in the status
-// word and the work it names is skipped, so a corrupted table becomes an
-// error status instead of an access out of bounds.
+// every kernel whose tables live in device memory (tile lists, problem and
+// work-item tables: the GEMM kernels and the first kernel) validates the indices
+// it reads from them against the sizes it was launched with before using them;
+// an invalid entry records MUON_ERR_INVALID_ARG in the status word and the work
+// it names is skipped, so a corrupted table becomes an error status instead of
+// an access out of bounds.  The AdamW and gradient kernels have no such table:
+// theirs is a kernel argument that the host fills from checked arguments in the
+// call itself.
 #ifdef MUON_BOUNDS_CHECK
 constexpr bool kBoundsCheck = true;
 #else
@@ -270,8 +273,8 @@ constexpr int GRAD_MAX_TENSORS = 512;                          // per launch
 constexpr int GRAD_MIDDLE_TENSORS = 256;
 constexpr int GRAD_SHORT_TENSORS = 64;
 constexpr int GRAD_MAX_CTAS = 148 * 8;                         // partial values of one launch
-// Of a list that is scaled, the part that the norm's reading leaves in L2: 64
-// MB.  Clipping GPT-2 124M (bf16 into fp32; fp32 in place) takes 174 and 250 us
+// Of a list (of one launch) that is scaled, the part that the norm's reading
+// leaves in L2: 64 MB.  Clipping GPT-2 124M (bf16 into fp32; fp32 in place) takes 174 and 250 us
 // without this, 170 and 240 us with 64 MB, 171 and 247 us with 96 MB.
 constexpr int GRAD_KEEP_CHUNKS = 2048;
 // Lists of at most GRAD_CLUSTER_CHUNKS chunks (1 MB) take the one-cluster kernel.
