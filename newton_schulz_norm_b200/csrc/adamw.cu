@@ -16,8 +16,8 @@
 // are the aligned ones that cover a tensor, so that one which starts off a
 // 16-byte boundary takes them too, if its four arrays are off by the same (as
 // views at one offset into flat buffers are); others take a scalar path with
-// the same arithmetic.  39.5e6 elements in 100 tensors: 186 us, 5.95 TB/s, with
-// and without a gradient scale; 30e6 elements one element off a boundary: 142
+// the same arithmetic.  39.5e6 elements in 100 tensors: 186-191 us (boxes differ),
+// 5.8-5.95 TB/s, with and without a gradient scale; 30e6 elements one element off a boundary: 142
 // us, as on it (208 us on the scalar path).
 #include "internal.h"
 

@@ -277,11 +277,13 @@ constexpr int GRAD_MAX_CTAS = 148 * 8;                         // partial values
 // leaves in L2: 64 MB.  Clipping GPT-2 124M (bf16 into fp32; fp32 in place) takes 174 and 250 us
 // without this, 170 and 240 us with 64 MB, 171 and 247 us with 96 MB.
 constexpr int GRAD_KEEP_CHUNKS = 2048;
-// Lists of at most GRAD_CLUSTER_CHUNKS chunks (1 MB) take the one-cluster kernel.
-// Through the binding the two launches of the other form take about 10.5 us of
-// host time, whatever they read; the cluster's one takes 7.1, and 4.6, 5.3, 6.2 us
-// on the device for the norm of 256 KB, 512 KB, 1 MB (clipped 6.2, 6.2, 10.2) but
-// 8.2 (14.3) for 2 MB.  CTAs of 1024 threads: 6.2, 6.2, 6.2 (8.2, 10.3, 10.3).
+// Lists of at most GRAD_CLUSTER_CHUNKS chunks (1 MB of one tensor; of many small
+// ones each counts a chunk) take the one-cluster kernel.  Through the binding the
+// two launches of the other form take about 10.5 us of host time, whatever they
+// read; the cluster's one takes 7.1.  Called from C in a row the norm of one tensor
+// of 256 KB, 512 KB, 1 MB takes 4.6, 5.3, 6.2 us (clipped 6.2, 6.2, 10.2), of 2 MB
+// 8.2 (14.3); CTAs of 1024 threads: 6.2, 6.2, 6.2 (8.2, 10.3, 10.3).  In a captured
+// graph the norm of 256 KB takes 3.5 us a call, clipped 5.4.
 constexpr int GRAD_CLUSTER_CHUNKS = 32;
 constexpr int GRAD_CLUSTER_THREADS = 512;
 constexpr int GRAD_CLUSTER_MAX = 8;                            // CTAs

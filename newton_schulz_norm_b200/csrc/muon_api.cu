@@ -399,10 +399,11 @@ std::vector<K1Info> k1_infos(const std::vector<Geom>& geom, const std::vector<lo
   long long tiles = 0;
   for (const Geom& g : geom) tiles += cdiv(g.r, K1_TILE) * cdiv(g.c, K1_TILE);
   // A small set is cut finer, so that every CTA of the launch gets an item.
-  // One 256 x 256 matrix: 20.8 instead of 25.1 us, three matrices with odd sides
-  // (129 x 1001 and the like) 24 instead of 31 us, four of 768 x 768 26 instead of
-  // 29 us; with two items for every CTA instead of one a GPT-2 block takes 39
-  // instead of 36 us.
+  // In a captured graph one 256 x 256 matrix takes 10.3 instead of 14.4 us, three
+  // with odd sides (129 x 1001, 1003 x 129, 130 x 130) 12.4 instead of 20.5 us, four
+  // of 768 x 768 16.3 instead of 18.4 us, a GPT-2 block 31.5 instead of 30.8 us;
+  // with two items for every CTA instead of one the block takes 37.7 us, the others
+  // what they take with one.
   int group = K1_GROUP;
   while (group > 1 && tiles < group * ctas) group /= 2;
   for (size_t i = 0; i < geom.size(); ++i) {
